@@ -456,6 +456,27 @@ NV4_API nv4_status nv4_hadamard2_nvfp4_quant(const void* w, nv4_dtype dt, int64_
                                      uint32_t* d_flags, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * nv4_linear_w4a16 -- the weight-only linear layer on NVFP4 weights ([CAL] layer table:
+ * W4A16 layers, activations kept in 16 bits).
+ *
+ *   out[t, n] = s2 * sum_k x[t, k] * e2m1(q[n, k]) * e4m3(scales[n, k/16])
+ *
+ * x      : [T, K] of dt (NV4_BF16 or NV4_FP16), leading dimension ldx >= K.
+ * q, scales, d_s2 : weights [N, K] as nv4_scale_sweep, nv4_weight_quant_rtn and
+ *          nv4_mxfp4_to_nvfp4 write them (codes [N, K/2], E4M3 block scales [N, K/16], one
+ *          FP32 scale on the device), contiguous.
+ * out    : [T, N] of out_dt (any nv4_dtype), leading dimension ldd >= N; 16-byte aligned base,
+ *          no rule for ldd.
+ * T is any number of rows (one decoded token to a prompt), N any, K a multiple of 16 (and
+ * K <= 65536, NV4_ERR_LIMIT beyond).  e2m1 * e4m3 is exact in the product's operands, sums are
+ * FP32, the result is rounded once to out_dt.  A NaN or Inf in x or a NaN scale propagates to
+ * the outputs that it reaches.  T == 0 or N == 0 is a no-op.
+ */
+NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, int64_t ldx,
+                            const uint8_t* q, const uint8_t* scales, const float* d_s2, int64_t N,
+                            nv4_dtype out_dt, void* out, int64_t ldd, uint32_t* d_flags, void* stream);
+
+/* ---------------------------------------------------------------------------
  * nv4_selftest -- checks, on the current device, the hardware FP4/FP8 conversion
  * instructions the kernels rely on (lane order, rounding, sign of zero, saturation).
  * Writes 64 uint32 results to d_out (device); d_out[0] is a bit mask of failed

@@ -29,6 +29,7 @@ __all__ = [
     "FLAG_OVERFLOW", "FLAG_TIMEOUT", "tensor_amax", "act_quant", "dequant", "hessian_accum",
     "scale_sweep", "mxfp4_to_nvfp4", "HessianJob", "SweepJob", "CastJob", "AmaxJob", "ActJob", "DequantJob",
     "nv4_tensor_amax_batched", "nv4_act_quant_batched", "nv4_dequant_batched", "nv4_weight_quant_rtn_batched",
+    "nv4_linear_w4a16", "linear_w4a16",
 ]
 
 BF16, FP16, FP32 = 0, 1, 2
@@ -95,6 +96,7 @@ _SIGS = {
     "nv4_hadamard_nvfp4_quant": (C.c_int, [_vp, _i64, _i64, _i64, C.c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "nv4_scales_to_mma_layout": (C.c_int, [_vp, _i64, _i64, _vp, _vp]),
     "nv4_gemm_nvfp4": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _i64, _vp, _vp]),
+    "nv4_linear_w4a16": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, C.c_int, _vp, _i64, _vp, _vp]),
     "nv4_hessian_accum": (C.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "nv4_hessian_accum_batched": (C.c_int, [C.POINTER(HessianJob), C.c_int, _vp, _vp]),
     "nv4_scale_sweep": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -693,3 +695,65 @@ def mxfp4_to_nvfp4(mx_q, e8m0, in_place=False, d_counts=None, d_flags=None, stre
     s2 = torch.empty((1,), dtype=torch.float32, device=dev)
     nv4_mxfp4_to_nvfp4(mx_q, e8m0, nv_q, nv_s, ga, s2, d_counts, d_flags, stream)
     return nv_q, nv_s, ga, s2
+
+
+# ------------------------------------------------------------------ products on FP4 weights
+def _here(x: torch.Tensor, *others):
+    """All tensors of a product live on the current device: the library launches there."""
+    if not x.is_cuda:
+        raise NV4Error("tensor must live on a CUDA device")
+    d = x.device
+    if d.index != torch.cuda.current_device():
+        raise NV4Error(f"tensors live on {d}: make it the current device (torch.cuda.device)")
+    for t in others:
+        if t is not None and t.device != d:
+            raise NV4Error(f"tensors live on different devices ({d}, {t.device})")
+
+
+def _new(shape, dtype, x: torch.Tensor, stream) -> torch.Tensor:
+    """An output allocated for the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=x.device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=x.device)
+
+
+def _f32_n(t: torch.Tensor, n: int, name: str):
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise NV4Error(f"{name} must be a contiguous float32 tensor of {n}")
+    return t.data_ptr()
+
+
+def _rows16(x: torch.Tensor, name: str):
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise NV4Error(f"{name} must be bf16 or float16")
+    rows, cols, ld = _rowmajor(x, name)
+    return rows, cols, max(ld, cols) if rows <= 1 else ld
+
+
+def nv4_linear_w4a16(x, q, scales, d_s2, out, d_flags=None, stream=None):
+    """out[t, n] = s2 * sum_k x[t, k] * W[n, k]: bf16 / float16 rows x [T, K], NVFP4 weights
+    (codes [N, K/2], E4M3 scales [N, K/16], s2)."""
+    _here(x, q, scales, d_s2, out, d_flags)
+    T, K, ldx = _rows16(x, "x")
+    if q.dim() != 2:
+        raise NV4Error("q must be [N, K/2]")
+    N = q.shape[0]
+    _u8(q, (N, K // 2), "q")
+    _u8(scales, (N, K // 16), "scales")
+    if out.dtype not in _DT:
+        raise NV4Error("out must be bf16, float16 or float32")
+    orows, ocols, ldd = _rowmajor(out, "out")
+    if (orows, ocols) != (T, N):
+        raise NV4Error("out must be [T, N]")
+    _check(lib().nv4_linear_w4a16(x.data_ptr(), _DT[x.dtype], T, K, ldx, q.data_ptr(), scales.data_ptr(),
+                                  _f32_n(d_s2, 1, "d_s2"), N, _DT[out.dtype], out.data_ptr(),
+                                  max(ldd, N) if T <= 1 else ldd, _ptr(d_flags), _stream(stream)), "nv4_linear_w4a16")
+
+
+def linear_w4a16(x, q, scales, d_s2, dtype=None, d_flags=None, stream=None):
+    """x [T, K] through NVFP4 weights [N, K] -> [T, N] of dtype (default: x's)."""
+    out = _new((x.shape[0], q.shape[0]), dtype or x.dtype, x, stream)
+    nv4_linear_w4a16(x, q, scales, d_s2, out, d_flags, stream)
+    return out

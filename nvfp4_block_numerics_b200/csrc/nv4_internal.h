@@ -86,6 +86,12 @@ cudaError_t launch_mma_scale_layout(const uint8_t* sc, int64_t rows, int64_t kb,
 cudaError_t launch_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa, const float* d_s2a, const uint8_t* qb,
                               const uint8_t* sfb, const float* d_s2b, int64_t M, int64_t N, int64_t K, int out_dt,
                               void* out, int64_t ldd, uint32_t* d_flags, cudaStream_t s);
+// K of one linear_w4a16 / mixture-of-experts call at most: one token row in shared memory.
+constexpr int64_t kMaxW4K = 65536;
+constexpr size_t kMaxSmemW4 = 220u * 1024u;
+cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
+                                const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
+                                cudaStream_t s);
 cudaError_t launch_dequant(const DequantTask* tasks, int n, int out_dt, cudaStream_t s);
 cudaError_t launch_hessian(const nv4_hessian_job* jobs, int n, uint32_t* d_flags, cudaStream_t s, int* bad_job);
 cudaError_t launch_sweep(const nv4_sweep_job* jobs, int n, int dt, uint32_t* d_flags, cudaStream_t s);

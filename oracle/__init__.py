@@ -412,6 +412,16 @@ def scales_to_mma_layout(sc: np.ndarray) -> np.ndarray:
     return out
 
 
+# ---------------------------------------------------------------- weight-only linear layer
+def linear_w4a16(x: np.ndarray, q: np.ndarray, sc: np.ndarray, s2: float):
+    """y[t, n] = sum_k x[t, k] * e2m1(q[n, k]) * e4m3(sc[n, k/16]) * s2 in FP64 for 16-bit rows
+    x given as float64 values ([CAL] layer table: W4A16).  Returns (y, yabs), yabs = |x| |W|^T,
+    the scale of the accumulation error."""
+    W = _dequant_exact(q, sc, s2)
+    x = np.asarray(x, np.float64)
+    return x @ W.T, np.abs(x) @ np.abs(W).T
+
+
 # ---------------------------------------------------------------- format variants
 def mxfp4_quant(x: np.ndarray, cols: int | None = None, threads: int | None = None):
     """MXFP4 round-to-nearest quantization ([FP4] sections 1.2 and 3.2): 32-element blocks,
