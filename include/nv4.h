@@ -477,6 +477,59 @@ NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int6
                             nv4_dtype out_dt, void* out, int64_t ldd, uint32_t* d_flags, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens on NVFP4 expert weights ([DSPARK], [CAST]
+ * section 3: routed experts w1, w3, w2; [CAL] layer table: W4A16).
+ *
+ * nv4_moe_route -- logits[t, e] = sum_h x[t, h] * w_router[e, h]; ids[t, 0..top_k) are the
+ * experts with the largest logits in descending order, ties to the lower index; weights[t, j] =
+ * softmax(logits[t])[ids[t, j]], divided by the sum of the chosen ones if renormalize != 0.
+ * The logits are formed in FP64 (the products of 16-bit values are exact, so the choice does not
+ * depend on the order of summation).  A NaN or Inf logit sets NV4_FLAG_NONFINITE; NaN ranks
+ * last, and that token's weights are unspecified.
+ *
+ * nv4_moe_experts -- out[t, :] = sum_j weights[t, j] * down_e ( silu(gate_e x_t) * (up_e x_t) ),
+ * e = ids[t, j], silu(z) = z / (1 + exp(-z)).  An id outside [0, E) is no expert and adds
+ * nothing (padded rows: out is 0 if a token has none); an id that a token names more than once
+ * counts with the sum of its weights.  The hidden values are FP32, rounded to FP16 relative to
+ * their row's largest magnitude for the down product; all sums are FP32; results do not depend
+ * on the order in which CTAs run.
+ *
+ * nv4_moe_layer -- both, one after the other.
+ *
+ * x        : [T, H] of dt (NV4_BF16 or NV4_FP16), leading dimension ldx >= H (ldx % 8 == 0).
+ * w_router : [E, H] of dt, contiguous.
+ * gate, up : codes [E, I, H/2], scales [E, I, H/16], d_s2 [E] (one FP32 scale per expert);
+ * down     : codes [E, H, I/2], scales [E, H, I/16], d_s2 [E]; all contiguous.
+ * ids      : int32 [T, top_k]; weights: float [T, top_k]; both contiguous.
+ * out      : [T, H] of out_dt, leading dimension ldd >= H, 16-byte aligned base.
+ * d_work   : nv4_moe_work_bytes(T, top_k, I) bytes, 16-byte aligned, not shared by calls that
+ *            may run at the same time; nothing has to be in it and nothing is kept in it.
+ * Limits (NV4_ERR_LIMIT beyond): T <= 64, T * top_k <= 2048, E <= 512, top_k <= min(32, E),
+ * H, I <= 32768.  H and I multiples of 16 (NV4_ERR_SHAPE).  T == 0 is a no-op.
+ */
+typedef struct {
+    const uint8_t* q;
+    const uint8_t* scales;
+    const float* d_s2;
+} nv4_expert_weights;
+
+NV4_API nv4_status nv4_moe_route(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx,
+                         const void* w_router, int64_t E, int top_k, int renormalize, int32_t* ids,
+                         float* weights, uint32_t* d_flags, void* stream);
+NV4_API size_t nv4_moe_work_bytes(int64_t T, int top_k, int64_t I);
+NV4_API nv4_status nv4_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx,
+                           const int32_t* ids, const float* weights, int top_k, int64_t E, int64_t I,
+                           const nv4_expert_weights* gate, const nv4_expert_weights* up,
+                           const nv4_expert_weights* down, nv4_dtype out_dt, void* out, int64_t ldd,
+                           void* d_work, size_t work_bytes, uint32_t* d_flags, void* stream);
+NV4_API nv4_status nv4_moe_layer(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx,
+                         const void* w_router, int64_t E, int top_k, int renormalize, int64_t I,
+                         const nv4_expert_weights* gate, const nv4_expert_weights* up,
+                         const nv4_expert_weights* down, int32_t* ids, float* weights, nv4_dtype out_dt,
+                         void* out, int64_t ldd, void* d_work, size_t work_bytes, uint32_t* d_flags,
+                         void* stream);
+
+/* ---------------------------------------------------------------------------
  * nv4_selftest -- checks, on the current device, the hardware FP4/FP8 conversion
  * instructions the kernels rely on (lane order, rounding, sign of zero, saturation).
  * Writes 64 uint32 results to d_out (device); d_out[0] is a bit mask of failed

@@ -29,7 +29,8 @@ __all__ = [
     "FLAG_OVERFLOW", "FLAG_TIMEOUT", "tensor_amax", "act_quant", "dequant", "hessian_accum",
     "scale_sweep", "mxfp4_to_nvfp4", "HessianJob", "SweepJob", "CastJob", "AmaxJob", "ActJob", "DequantJob",
     "nv4_tensor_amax_batched", "nv4_act_quant_batched", "nv4_dequant_batched", "nv4_weight_quant_rtn_batched",
-    "nv4_linear_w4a16", "linear_w4a16",
+    "nv4_linear_w4a16", "linear_w4a16", "nv4_moe_route", "nv4_moe_work_bytes", "nv4_moe_experts", "nv4_moe_layer",
+    "moe_route", "moe_experts", "moe_layer", "ExpertWeights",
 ]
 
 BF16, FP16, FP32 = 0, 1, 2
@@ -66,6 +67,10 @@ class CastJob(C.Structure):
                 ("nv_scales", _vp), ("d_global_amax", _vp), ("d_s2", _vp), ("group", C.c_int32)]
 
 
+class ExpertWeights(C.Structure):
+    _fields_ = [("q", _vp), ("scales", _vp), ("d_s2", _vp)]
+
+
 class NV4Error(RuntimeError):
     pass
 
@@ -97,6 +102,14 @@ _SIGS = {
     "nv4_scales_to_mma_layout": (C.c_int, [_vp, _i64, _i64, _vp, _vp]),
     "nv4_gemm_nvfp4": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _i64, _vp, _vp]),
     "nv4_linear_w4a16": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, C.c_int, _vp, _i64, _vp, _vp]),
+    "nv4_moe_route": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _i64, C.c_int, C.c_int, _vp, _vp, _vp, _vp]),
+    "nv4_moe_work_bytes": (C.c_size_t, [_i64, C.c_int, _i64]),
+    "nv4_moe_experts": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, C.c_int, _i64, _i64,
+                                  C.POINTER(ExpertWeights), C.POINTER(ExpertWeights), C.POINTER(ExpertWeights), C.c_int,
+                                  _vp, _i64, _vp, C.c_size_t, _vp, _vp]),
+    "nv4_moe_layer": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _i64, C.c_int, C.c_int, _i64,
+                                C.POINTER(ExpertWeights), C.POINTER(ExpertWeights), C.POINTER(ExpertWeights), _vp, _vp,
+                                C.c_int, _vp, _i64, _vp, C.c_size_t, _vp, _vp]),
     "nv4_hessian_accum": (C.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "nv4_hessian_accum_batched": (C.c_int, [C.POINTER(HessianJob), C.c_int, _vp, _vp]),
     "nv4_scale_sweep": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -757,3 +770,108 @@ def linear_w4a16(x, q, scales, d_s2, dtype=None, d_flags=None, stream=None):
     out = _new((x.shape[0], q.shape[0]), dtype or x.dtype, x, stream)
     nv4_linear_w4a16(x, q, scales, d_s2, out, d_flags, stream)
     return out
+
+
+def _expert_weights(w, E: int, rows: int, cols: int, name: str) -> ExpertWeights:
+    """(codes [E, rows, cols/2], scales [E, rows, cols/16], s2 [E]) of one matrix per expert."""
+    q, sc, s2 = w
+    _u8(q, (E, rows, cols // 2), f"{name} codes")
+    _u8(sc, (E, rows, cols // 16), f"{name} scales")
+    return ExpertWeights(q.data_ptr(), sc.data_ptr(), _f32_n(s2, E, f"{name} s2"))
+
+
+def _routing(ids, weights, T: int):
+    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+        raise NV4Error("ids must be a contiguous int32 tensor [T, top_k]")
+    if weights.dtype != torch.float32 or weights.shape != ids.shape or not weights.is_contiguous():
+        raise NV4Error("weights must be a contiguous float32 tensor [T, top_k]")
+    return ids.shape[1]
+
+
+def _router(w_router, x):
+    if w_router.dtype != x.dtype or w_router.dim() != 2 or w_router.shape[1] != x.shape[1] or not w_router.is_contiguous():
+        raise NV4Error("w_router must be a contiguous tensor [E, H] of x's type")
+    return w_router.shape[0]
+
+
+def _moe_shapes(x, gate, down, out, work, k: int):
+    T, H, ldx = _rows16(x, "x")
+    if gate[0].dim() != 3:
+        raise NV4Error("gate codes must be [E, I, H/2]")
+    E, I = gate[0].shape[:2]
+    if out.dtype not in _DT:
+        raise NV4Error("out must be bf16, float16 or float32")
+    orows, ocols, ldd = _rowmajor(out, "out")
+    if (orows, ocols) != (T, H):
+        raise NV4Error("out must be [T, H]")
+    if not work.is_contiguous() or work.numel() * work.element_size() < nv4_moe_work_bytes(T, k, I):
+        raise NV4Error(f"work must be a contiguous tensor of at least {nv4_moe_work_bytes(T, k, I)} bytes")
+    return T, H, ldx, E, I, max(ldd, H) if T <= 1 else ldd
+
+
+def nv4_moe_work_bytes(T: int, top_k: int, I: int) -> int:
+    return int(lib().nv4_moe_work_bytes(T, top_k, I))
+
+
+def nv4_moe_route(x, w_router, ids, weights, renormalize=True, d_flags=None, stream=None):
+    """ids, weights [T, top_k]: the experts of the largest router logits and their softmax weights."""
+    _here(x, w_router, ids, weights, d_flags)
+    T, H, ldx = _rows16(x, "x")
+    E, k = _router(w_router, x), _routing(ids, weights, T)
+    _check(lib().nv4_moe_route(x.data_ptr(), _DT[x.dtype], T, H, ldx, w_router.data_ptr(), E, k, int(bool(renormalize)),
+                               ids.data_ptr(), weights.data_ptr(), _ptr(d_flags), _stream(stream)), "nv4_moe_route")
+
+
+def nv4_moe_experts(x, ids, weights, gate, up, down, out, work, d_flags=None, stream=None):
+    """out[t] = sum_j weights[t, j] * down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j]; gate, up and
+    down: (codes, scales, s2) of every expert's matrix; work: nv4_moe_work_bytes(T, top_k, I) bytes."""
+    _here(x, ids, weights, *gate, *up, *down, out, work, d_flags)
+    k = _routing(ids, weights, x.shape[0])
+    T, H, ldx, E, I, ldd = _moe_shapes(x, gate, down, out, work, k)
+    g, u, d = (_expert_weights(gate, E, I, H, "gate"), _expert_weights(up, E, I, H, "up"),
+               _expert_weights(down, E, H, I, "down"))
+    _check(lib().nv4_moe_experts(x.data_ptr(), _DT[x.dtype], T, H, ldx, ids.data_ptr(), weights.data_ptr(), k, E, I,
+                                 g, u, d, _DT[out.dtype], out.data_ptr(), ldd, work.data_ptr(),
+                                 work.numel() * work.element_size(), _ptr(d_flags), _stream(stream)), "nv4_moe_experts")
+
+
+def nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize=True, d_flags=None, stream=None):
+    """nv4_moe_route into ids and weights, then nv4_moe_experts."""
+    _here(x, w_router, *gate, *up, *down, ids, weights, out, work, d_flags)
+    k = _routing(ids, weights, x.shape[0])
+    T, H, ldx, E, I, ldd = _moe_shapes(x, gate, down, out, work, k)
+    if _router(w_router, x) != E:
+        raise NV4Error("w_router must have a row per expert")
+    g, u, d = (_expert_weights(gate, E, I, H, "gate"), _expert_weights(up, E, I, H, "up"),
+               _expert_weights(down, E, H, I, "down"))
+    _check(lib().nv4_moe_layer(x.data_ptr(), _DT[x.dtype], T, H, ldx, w_router.data_ptr(), E, k, int(bool(renormalize)),
+                               I, g, u, d, ids.data_ptr(), weights.data_ptr(), _DT[out.dtype], out.data_ptr(), ldd,
+                               work.data_ptr(), work.numel() * work.element_size(), _ptr(d_flags), _stream(stream)),
+           "nv4_moe_layer")
+
+
+def moe_route(x, w_router, top_k: int, renormalize=True, d_flags=None, stream=None):
+    """x [T, H], w_router [E, H] -> (ids int32 [T, top_k], weights float32 [T, top_k])."""
+    ids = _new((x.shape[0], top_k), torch.int32, x, stream)
+    weights = _new((x.shape[0], top_k), torch.float32, x, stream)
+    nv4_moe_route(x, w_router, ids, weights, renormalize, d_flags, stream)
+    return ids, weights
+
+
+def moe_experts(x, ids, weights, gate, up, down, dtype=None, d_flags=None, stream=None):
+    """x [T, H] through the chosen experts -> [T, H] of dtype (default: x's)."""
+    out = _new(tuple(x.shape), dtype or x.dtype, x, stream)
+    work = _new((ids.numel() * gate[0].shape[1],), torch.float32, x, stream)
+    nv4_moe_experts(x, ids, weights, gate, up, down, out, work, d_flags, stream)
+    return out
+
+
+def moe_layer(x, w_router, gate, up, down, top_k: int, renormalize=True, dtype=None, d_flags=None, stream=None):
+    """The whole layer: x [T, H] -> (out [T, H], ids, weights)."""
+    T = x.shape[0]
+    out = _new(tuple(x.shape), dtype or x.dtype, x, stream)
+    ids = _new((T, top_k), torch.int32, x, stream)
+    weights = _new((T, top_k), torch.float32, x, stream)
+    work = _new((T * top_k * gate[0].shape[1],), torch.float32, x, stream)
+    nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize, d_flags, stream)
+    return out, ids, weights

@@ -531,6 +531,96 @@ nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, i
                                          (cudaStream_t)stream));
 }
 
+// ------------------------------------------------------------------ mixture of experts
+static nv4_status check_moe_rows(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, int64_t E, int top_k)
+{
+    if (dt != NV4_BF16 && dt != NV4_FP16) return NV4_ERR_DTYPE;
+    if (T < 0 || H <= 0 || H % 16 != 0 || ldx < H || E <= 0 || top_k <= 0 || top_k > E) return NV4_ERR_SHAPE;
+    if (T > kMaxMoeTokens || E > kMaxMoeExperts || top_k > kMaxMoeTopK || T * top_k > kMaxMoePairs || H > kMaxMoeWidth)
+        return NV4_ERR_LIMIT;
+    if (T == 0) return NV4_OK;
+    if (x == nullptr) return NV4_ERR_NULL;
+    if (!aligned16(x) || ldx % 8 != 0) return NV4_ERR_ALIGN;
+    return NV4_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0u; }
+
+static nv4_status check_moe_experts(int64_t T, int64_t H, int64_t I, const nv4_expert_weights* const w[3],
+                                    const int32_t* ids, const float* weights, int top_k, nv4_dtype out_dt, const void* out,
+                                    int64_t ldd, const void* work, size_t work_bytes)
+{
+    if (out_dt != NV4_BF16 && out_dt != NV4_FP16 && out_dt != NV4_FP32) return NV4_ERR_DTYPE;
+    if (I <= 0 || I % 16 != 0 || ldd < H) return NV4_ERR_SHAPE;
+    if (I > kMaxMoeWidth) return NV4_ERR_LIMIT;
+    if (T == 0) return NV4_OK;
+    if (ids == nullptr || weights == nullptr || out == nullptr || work == nullptr) return NV4_ERR_NULL;
+    for (int i = 0; i < 3; ++i)
+        if (w[i] == nullptr || w[i]->q == nullptr || w[i]->scales == nullptr || w[i]->d_s2 == nullptr) return NV4_ERR_NULL;
+    for (int i = 0; i < 3; ++i)
+        if (!aligned16(w[i]->q) || !aligned16(w[i]->scales) || !aligned4(w[i]->d_s2)) return NV4_ERR_ALIGN;
+    if (!aligned16(out) || !aligned16(work) || !aligned4(ids) || !aligned4(weights)) return NV4_ERR_ALIGN;
+    if (work_bytes < nv4_moe_work_bytes(T, top_k, I)) return NV4_ERR_LIMIT;
+    return NV4_OK;
+}
+
+static nv4_status run_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
+                                  const float* weights, int top_k, int64_t E, int64_t I,
+                                  const nv4_expert_weights* const w[3], nv4_dtype out_dt, void* out, int64_t ldd,
+                                  void* work, void* stream)
+{
+    const MoeExpertsArgs a{x, (int)dt, (int)out_dt, T, top_k, E, H, I, ldx, ldd, ids, weights, w[0]->q, w[0]->scales,
+                           w[1]->q, w[1]->scales, w[2]->q, w[2]->scales, w[0]->d_s2, w[1]->d_s2, w[2]->d_s2,
+                           static_cast<float*>(work), out};
+    return from_cuda(launch_moe_experts(a, (cudaStream_t)stream));
+}
+
+nv4_status nv4_moe_route(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const void* w_router,
+                         int64_t E, int top_k, int renormalize, int32_t* ids, float* weights, uint32_t* d_flags,
+                         void* stream)
+{
+    const nv4_status st = check_moe_rows(x, dt, T, H, ldx, E, top_k);
+    if (st != NV4_OK || T == 0) return st;
+    if (w_router == nullptr || ids == nullptr || weights == nullptr) return NV4_ERR_NULL;
+    if (!aligned16(w_router) || !aligned4(ids) || !aligned4(weights)) return NV4_ERR_ALIGN;
+    return from_cuda(launch_moe_route(x, (int)dt, T, H, ldx, w_router, E, top_k, renormalize != 0, ids, weights,
+                                      d_flags, (cudaStream_t)stream));
+}
+
+size_t nv4_moe_work_bytes(int64_t T, int top_k, int64_t I)
+{
+    if (T <= 0 || top_k <= 0 || I <= 0) return 0;
+    return (size_t)T * (size_t)top_k * (size_t)I * sizeof(float);
+}
+
+nv4_status nv4_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
+                           const float* weights, int top_k, int64_t E, int64_t I, const nv4_expert_weights* gate,
+                           const nv4_expert_weights* up, const nv4_expert_weights* down, nv4_dtype out_dt, void* out,
+                           int64_t ldd, void* d_work, size_t work_bytes, uint32_t* d_flags, void* stream)
+{
+    (void)d_flags;
+    const nv4_expert_weights* const w[3] = {gate, up, down};
+    nv4_status st = check_moe_rows(x, dt, T, H, ldx, E, top_k);
+    if (st == NV4_OK) st = check_moe_experts(T, H, I, w, ids, weights, top_k, out_dt, out, ldd, d_work, work_bytes);
+    if (st != NV4_OK || T == 0) return st;
+    return run_moe_experts(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work, stream);
+}
+
+nv4_status nv4_moe_layer(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const void* w_router,
+                         int64_t E, int top_k, int renormalize, int64_t I, const nv4_expert_weights* gate,
+                         const nv4_expert_weights* up, const nv4_expert_weights* down, int32_t* ids, float* weights,
+                         nv4_dtype out_dt, void* out, int64_t ldd, void* d_work, size_t work_bytes, uint32_t* d_flags,
+                         void* stream)
+{
+    const nv4_expert_weights* const w[3] = {gate, up, down};
+    nv4_status st = check_moe_rows(x, dt, T, H, ldx, E, top_k);
+    if (st == NV4_OK) st = check_moe_experts(T, H, I, w, ids, weights, top_k, out_dt, out, ldd, d_work, work_bytes);
+    if (st != NV4_OK || T == 0) return st;
+    st = nv4_moe_route(x, dt, T, H, ldx, w_router, E, top_k, renormalize, ids, weights, d_flags, stream);
+    if (st != NV4_OK) return st;
+    return run_moe_experts(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work, stream);
+}
+
 // ------------------------------------------------------------------ format variants
 nv4_status nv4_mxfp4_quant(const void* x, nv4_dtype dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
                            uint8_t* e8m0, uint32_t* d_flags, void* stream)

@@ -92,6 +92,25 @@ constexpr size_t kMaxSmemW4 = 220u * 1024u;
 cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
                                 cudaStream_t s);
+// Mixture-of-experts limits: tokens and (token, expert) pairs of a call, experts, experts per
+// token, widths (a token row of K <= 32768 beside the partial sums in shared memory).
+constexpr int64_t kMaxMoeTokens = 64, kMaxMoePairs = 2048, kMaxMoeExperts = 512, kMaxMoeTopK = 32;
+constexpr int64_t kMaxMoeWidth = 32768;
+constexpr size_t kMaxSmemMoe = 208u * 1024u;
+struct MoeExpertsArgs {
+    const void* x;
+    int dt, out_dt;
+    int64_t T, k, E, H, I, ldx, ldd;
+    const int32_t* ids;
+    const float* weights;
+    const uint8_t *gq, *gs, *uq, *us, *dq, *ds;
+    const float *g2, *u2, *d2;
+    float* h;
+    void* out;
+};
+cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_t ldx, const void* wr, int64_t E,
+                             int top_k, int renorm, int32_t* ids, float* weights, uint32_t* d_flags, cudaStream_t s);
+cudaError_t launch_moe_experts(const MoeExpertsArgs& a, cudaStream_t s);
 cudaError_t launch_dequant(const DequantTask* tasks, int n, int out_dt, cudaStream_t s);
 cudaError_t launch_hessian(const nv4_hessian_job* jobs, int n, uint32_t* d_flags, cudaStream_t s, int* bad_job);
 cudaError_t launch_sweep(const nv4_sweep_job* jobs, int n, int dt, uint32_t* d_flags, cudaStream_t s);

@@ -422,6 +422,46 @@ def linear_w4a16(x: np.ndarray, q: np.ndarray, sc: np.ndarray, s2: float):
     return x @ W.T, np.abs(x) @ np.abs(W).T
 
 
+# ---------------------------------------------------------------- mixture of experts
+def moe_route(x: np.ndarray, w_router: np.ndarray, top_k: int, renormalize: bool = True):
+    """Router of a mixture-of-experts layer in FP64: logits = x w_router^T, the top_k largest per
+    row (ties: the lower index), softmax weights (divided by their sum if renormalize).  x, w_router:
+    values as float64.  Returns (ids int32, weights float64)."""
+    logits = np.asarray(x, np.float64) @ np.asarray(w_router, np.float64).T
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
+    p = np.exp(logits - logits.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    w = np.take_along_axis(p, ids, 1)
+    return ids.astype(np.int32), (w / w.sum(1, keepdims=True) if renormalize else w)
+
+
+def moe_experts(x: np.ndarray, ids: np.ndarray, weights: np.ndarray, gate, up, down):
+    """out[t] = sum_j weights[t, j] down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j] ([DSPARK],
+    [CAST] section 3: routed experts in NVFP4), in FP64.  gate, up, down: (q, scales, s2) stacked
+    over the experts; an id outside [0, E) adds nothing.  Returns (out, dev): dev bounds the first
+    order effect on out of a relative error u in every hidden value and every accumulated product,
+    per unit u."""
+    x = np.asarray(x, np.float64)
+    out = np.zeros((x.shape[0], down[0].shape[1]))
+    dev = np.zeros_like(out)
+    E = gate[0].shape[0]
+    for e in sorted({int(i) for i in ids.ravel() if 0 <= i < E}):
+        G, U, D = (_dequant_exact(w[0][e], w[1][e], float(w[2][e])) for w in (gate, up, down))
+        for t in range(x.shape[0]):
+            w = float(sum(weights[t, j] for j in range(ids.shape[1]) if ids[t, j] == e))
+            if not np.any(ids[t] == e):
+                continue
+            g, u = G @ x[t], U @ x[t]
+            ga, ua = np.abs(G) @ np.abs(x[t]), np.abs(U) @ np.abs(x[t])
+            s = 1.0 / (1.0 + np.exp(-g))
+            h = g * s * u
+            # d silu / d g is at most 1.1 in magnitude
+            dh = 1.1 * ga * np.abs(u) + np.abs(g * s) * ua + np.abs(h)
+            out[t] += w * (D @ h)
+            dev[t] += abs(w) * (np.abs(D) @ (dh + np.abs(h)))
+    return out, dev
+
+
 # ---------------------------------------------------------------- format variants
 def mxfp4_quant(x: np.ndarray, cols: int | None = None, threads: int | None = None):
     """MXFP4 round-to-nearest quantization ([FP4] sections 1.2 and 3.2): 32-element blocks,

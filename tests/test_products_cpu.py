@@ -42,3 +42,56 @@ def test_linear_w4a16_oracle_is_the_dequantized_product(orc):
                 c = (int(q[n, k // 2]) >> (4 * (k % 2))) & 15
                 s += x[t, k] * orc.e2m1_value(c) * orc.e4m3_value(int(sc[n, k // 16])) * 0.25
             assert abs(s - y[t, n]) < 1e-9 * (1 + abs(s))
+
+
+def test_moe_refusals(L):
+    import ctypes as C
+
+    from nvfp4_block_numerics_b200 import binding as b
+
+    def route(x=FAKE, dt=0, T=2, H=64, ldx=64, wr=FAKE, E=8, k=2, ids=FAKE, w=FAKE):
+        return L.nv4_moe_route(x, dt, T, H, ldx, wr, E, k, 1, ids, w, None, None)
+
+    assert route(dt=2) == 4
+    assert route(H=40, ldx=40) == 2 and route(ldx=48) == 2 and route(k=9) == 2 and route(k=0) == 2 and route(E=0) == 2
+    assert route(T=65) == 6 and route(E=513) == 6 and route(E=64, k=33) == 6 and route(H=32784, ldx=32784) == 6
+    assert route(x=None) == 1 and route(wr=None) == 1 and route(ids=None) == 1 and route(w=None) == 1
+    assert route(x=FAKE + 2) == 3 and route(ldx=68) == 3 and route(wr=FAKE + 8) == 3 and route(ids=FAKE + 2) == 3
+    assert route(T=0) == 0
+
+    ok = b.ExpertWeights(FAKE, FAKE, FAKE)
+
+    def experts(x=FAKE, dt=0, T=2, H=64, ldx=64, ids=FAKE, w=FAKE, k=2, E=8, I=32, g=ok, u=ok, d=ok, odt=0, out=FAKE,
+                ldd=64, work=FAKE, wb=1 << 20):
+        P = lambda v: None if v is None else C.byref(v)  # noqa: E731
+        return L.nv4_moe_experts(x, dt, T, H, ldx, ids, w, k, E, I, P(g), P(u), P(d), odt, out, ldd, work, wb, None, None)
+
+    assert experts(dt=2) == 4 and experts(odt=5) == 4
+    assert experts(I=24) == 2 and experts(I=0) == 2 and experts(ldd=63) == 2 and experts(k=9) == 2
+    assert experts(I=32784) == 6 and experts(T=65) == 6 and experts(wb=2 * 2 * 32 * 4 - 1) == 6
+    assert experts(g=None) == 1 and experts(u=b.ExpertWeights(None, FAKE, FAKE)) == 1 and experts(work=None) == 1
+    assert experts(d=b.ExpertWeights(FAKE, FAKE + 4, FAKE)) == 3 and experts(work=FAKE + 8) == 3 and experts(out=FAKE + 2) == 3
+    assert experts(T=0) == 0
+    assert L.nv4_moe_work_bytes(3, 4, 32) == 3 * 4 * 32 * 4 and L.nv4_moe_work_bytes(0, 4, 32) == 0
+    # the whole layer refuses before it launches anything
+    assert L.nv4_moe_layer(FAKE, 0, 2, 64, 64, FAKE, 8, 2, 1, 24, C.byref(ok), C.byref(ok), C.byref(ok), FAKE, FAKE, 0, FAKE,
+                           64, FAKE, 1 << 20, None, None) == 2
+
+
+def test_moe_oracle_small(orc):
+    """One expert of weight 1 is the plain gated MLP; two experts add with their weights; an id
+    outside the range adds nothing."""
+    rng = np.random.default_rng(2)
+    mk = lambda E, r, c: (rng.integers(0, 256, (E, r, c // 2), dtype=np.uint8),  # noqa: E731
+                          rng.integers(0x30, 0x40, (E, r, c // 16), dtype=np.uint8), np.full(E, 0.01, np.float32))
+    gate, up, down = mk(3, 32, 16), mk(3, 32, 16), mk(3, 16, 32)
+    x = rng.standard_normal((1, 16))
+    one = lambda e: orc.moe_experts(x, np.array([[e]]), np.ones((1, 1)), gate, up, down)[0]  # noqa: E731
+    W = [orc._dequant_exact(w[0][1], w[1][1], float(w[2][1])) for w in (gate, up, down)]
+    g, u = W[0] @ x[0], W[1] @ x[0]
+    assert np.allclose(one(1)[0], W[2] @ (g / (1 + np.exp(-g)) * u), rtol=1e-12)
+    two, _ = orc.moe_experts(x, np.array([[2, 0]]), np.array([[0.25, 0.5]]), gate, up, down)
+    assert np.allclose(two, 0.25 * one(2) + 0.5 * one(0), rtol=1e-12)
+    assert np.all(one(-1) == 0) and np.all(one(3) == 0)
+    ids, w = orc.moe_route(np.array([[1.0, 0.0]]), np.array([[0.0, 1.0], [2.0, 0.0], [2.0, 0.0]]), 2)
+    assert ids.tolist() == [[1, 2]] and np.allclose(w, 0.5)
