@@ -456,6 +456,30 @@ NV4_API nv4_status nv4_hadamard2_nvfp4_quant(const void* w, nv4_dtype dt, int64_
                                      uint32_t* d_flags, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * MXFP4 x MXFP4 product on the block-scaled tensor cores ([FP4] 1.2, 4.1: 32-element E8M0
+ * blocks, scale factors reorganized for tcgen05.mma).
+ *
+ * nv4_mxfp4_quant_mma -- nv4_mxfp4_quant with the E8M0 codes written in the layout that the MMA
+ * reads: what nv4_scales_to_mma_layout makes of them, 512-byte atoms of 128 rows x 4 blocks (128
+ * K-elements), padding zeroed.  e8m0_mma: nv4_mxfp4_mma_scale_bytes(rows, cols) bytes, 16-byte
+ * aligned.  (Row-major codes [rows, cols/32] are rearranged by nv4_scales_to_mma_layout with
+ * cols / 2 as its cols.)
+ *
+ * nv4_gemm_mxfp4 -- D[m, n] = sum_k A[m, k] * B[n, k], A [M, K] and B [N, K] MXFP4: packed codes
+ * [rows, K/2] (contiguous, 16-byte aligned) and E8M0 scales in the MMA layout; value =
+ * e2m1 * 2^(e8m0 - 127).  Products are exact, accumulation is FP32 on the tensor cores; out
+ * (NV4_BF16 or NV4_FP32, [M, N], leading dimension ldd >= N, 16-byte aligned base) is rounded
+ * once.  M and N are any, K a multiple of 32.  A scale code 0xFF (NaN) makes its row's (A) or
+ * column's (B) outputs NaN.  M == 0 or N == 0 is a no-op.
+ */
+NV4_API size_t nv4_mxfp4_mma_scale_bytes(int64_t rows, int64_t cols);
+NV4_API nv4_status nv4_mxfp4_quant_mma(const void* x, nv4_dtype dt, int64_t rows, int64_t cols, int64_t ld,
+                               uint8_t* q, uint8_t* e8m0_mma, uint32_t* d_flags, void* stream);
+NV4_API nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8_t* qb,
+                          const uint8_t* sfb_mma, int64_t M, int64_t N, int64_t K, nv4_dtype out_dt,
+                          void* out, int64_t ldd, uint32_t* d_flags, void* stream);
+
+/* ---------------------------------------------------------------------------
  * nv4_linear_w4a16 -- the weight-only linear layer on NVFP4 weights ([CAL] layer table:
  * W4A16 layers, activations kept in 16 bits).
  *

@@ -30,7 +30,8 @@ __all__ = [
     "scale_sweep", "mxfp4_to_nvfp4", "HessianJob", "SweepJob", "CastJob", "AmaxJob", "ActJob", "DequantJob",
     "nv4_tensor_amax_batched", "nv4_act_quant_batched", "nv4_dequant_batched", "nv4_weight_quant_rtn_batched",
     "nv4_linear_w4a16", "linear_w4a16", "nv4_moe_route", "nv4_moe_work_bytes", "nv4_moe_experts", "nv4_moe_layer",
-    "moe_route", "moe_experts", "moe_layer", "ExpertWeights",
+    "moe_route", "moe_experts", "moe_layer", "ExpertWeights", "nv4_mxfp4_mma_scale_bytes", "nv4_mxfp4_quant_mma",
+    "nv4_gemm_mxfp4", "mxfp4_quant_mma", "gemm_mxfp4", "linear_mxfp4",
 ]
 
 BF16, FP16, FP32 = 0, 1, 2
@@ -102,6 +103,9 @@ _SIGS = {
     "nv4_scales_to_mma_layout": (C.c_int, [_vp, _i64, _i64, _vp, _vp]),
     "nv4_gemm_nvfp4": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _i64, _vp, _vp]),
     "nv4_linear_w4a16": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, C.c_int, _vp, _i64, _vp, _vp]),
+    "nv4_mxfp4_mma_scale_bytes": (C.c_size_t, [_i64, _i64]),
+    "nv4_mxfp4_quant_mma": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "nv4_gemm_mxfp4": (C.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _i64, _vp, _vp]),
     "nv4_moe_route": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _i64, C.c_int, C.c_int, _vp, _vp, _vp, _vp]),
     "nv4_moe_work_bytes": (C.c_size_t, [_i64, C.c_int, _i64]),
     "nv4_moe_experts": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, C.c_int, _i64, _i64,
@@ -875,3 +879,66 @@ def moe_layer(x, w_router, gate, up, down, top_k: int, renormalize=True, dtype=N
     work = _new((T * top_k * gate[0].shape[1],), torch.float32, x, stream)
     nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize, d_flags, stream)
     return out, ids, weights
+
+
+def nv4_mxfp4_mma_scale_bytes(rows: int, cols: int) -> int:
+    return int(lib().nv4_mxfp4_mma_scale_bytes(rows, cols))
+
+
+def _mma_bytes(t, rows: int, cols: int, name: str):
+    need = nv4_mxfp4_mma_scale_bytes(rows, cols)
+    if t.dtype != torch.uint8 or t.numel() < need or not t.is_contiguous():
+        raise NV4Error(f"{name} must be a contiguous uint8 tensor of at least nv4_mxfp4_mma_scale_bytes = {need} bytes")
+
+
+def nv4_mxfp4_quant_mma(x, q, e8m0_mma, d_flags=None, stream=None):
+    """MXFP4 of x [rows, cols] (bf16 or float32): codes [rows, cols/2] and scales in the MMA layout."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise NV4Error("x must be bf16 or float32")
+    _here(x, q, e8m0_mma, d_flags)
+    rows, cols, ld = _rowmajor(x, "x")
+    _u8(q, (rows, cols // 2), "q")
+    _mma_bytes(e8m0_mma, rows, cols, "e8m0_mma")
+    _check(lib().nv4_mxfp4_quant_mma(x.data_ptr(), _DT[x.dtype], rows, cols, max(ld, cols) if rows <= 1 else ld,
+                                     q.data_ptr(), e8m0_mma.data_ptr(), _ptr(d_flags), _stream(stream)),
+           "nv4_mxfp4_quant_mma")
+
+
+def nv4_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, out, d_flags=None, stream=None):
+    """out[M, N] = A @ B^T for MXFP4 operands (codes [rows, K/2], E8M0 scales in the MMA layout)."""
+    _here(qa, sfa_mma, qb, sfb_mma, out, d_flags)
+    M, half = qa.shape
+    N, K = qb.shape[0], 2 * half
+    _u8(qa, (M, half), "qa")
+    _u8(qb, (N, half), "qb")
+    _mma_bytes(sfa_mma, M, K, "sfa_mma")
+    _mma_bytes(sfb_mma, N, K, "sfb_mma")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise NV4Error("out must be bf16 or float32")
+    orows, ocols, ldd = _rowmajor(out, "out")
+    if (orows, ocols) != (M, N):
+        raise NV4Error("out must be [M, N]")
+    _check(lib().nv4_gemm_mxfp4(qa.data_ptr(), sfa_mma.data_ptr(), qb.data_ptr(), sfb_mma.data_ptr(), M, N, K,
+                                _DT[out.dtype], out.data_ptr(), max(ldd, N) if M <= 1 else ldd, _ptr(d_flags),
+                                _stream(stream)), "nv4_gemm_mxfp4")
+
+
+def mxfp4_quant_mma(x, d_flags=None, stream=None):
+    rows, cols = x.shape
+    q = _new((rows, cols // 2), torch.uint8, x, stream)
+    sf = _new((nv4_mxfp4_mma_scale_bytes(rows, cols),), torch.uint8, x, stream)
+    nv4_mxfp4_quant_mma(x, q, sf, d_flags, stream)
+    return q, sf
+
+
+def gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, dtype=torch.bfloat16, d_flags=None, stream=None):
+    out = _new((qa.shape[0], qb.shape[0]), dtype, qa, stream)
+    nv4_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, out, d_flags, stream)
+    return out
+
+
+def linear_mxfp4(x, qw, sfw_mma, dtype=torch.bfloat16, d_flags=None, stream=None):
+    """The W4A4 linear layer: x [M, K] quantized to MXFP4, times MXFP4 weights [N, K] (codes, scales
+    in the MMA layout) -> [M, N]."""
+    q, sf = mxfp4_quant_mma(x, d_flags, stream)
+    return gemm_mxfp4(q, sf, qw, sfw_mma, dtype, d_flags, stream)

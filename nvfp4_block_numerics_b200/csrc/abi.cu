@@ -513,6 +513,44 @@ nv4_status nv4_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa_mma, const float
                                        d_flags, (cudaStream_t)stream));
 }
 
+// ------------------------------------------------------------------ MXFP4 product
+size_t nv4_mxfp4_mma_scale_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || cols % 32 != 0) return 0;
+    return mma_scale_bytes(rows, cols / 32);
+}
+
+nv4_status nv4_mxfp4_quant_mma(const void* x, nv4_dtype dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
+                               uint8_t* e8m0_mma, uint32_t* d_flags, void* stream)
+{
+    if (dt != NV4_BF16 && dt != NV4_FP32) return NV4_ERR_DTYPE;
+    if (rows < 0 || cols < 0 || cols % 32 != 0 || ld < cols) return NV4_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return NV4_OK;
+    if (x == nullptr || q == nullptr || e8m0_mma == nullptr) return NV4_ERR_NULL;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(e8m0_mma) || ld % (dt == NV4_BF16 ? 8 : 4) != 0) return NV4_ERR_ALIGN;
+    if (rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 31 ||
+        (rows + 127) / 128 * 128 * ((cols + 127) / 128) >= (int64_t)1 << 28)
+        return NV4_ERR_LIMIT;
+    return from_cuda(launch_mxfp4_quant_mma(x, dt == NV4_BF16 ? 0 : 2, rows, cols, ld, q, e8m0_mma, d_flags,
+                                            (cudaStream_t)stream));
+}
+
+nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8_t* qb, const uint8_t* sfb_mma, int64_t M,
+                          int64_t N, int64_t K, nv4_dtype out_dt, void* out, int64_t ldd, uint32_t* d_flags, void* stream)
+{
+    if (out_dt != NV4_BF16 && out_dt != NV4_FP32) return NV4_ERR_DTYPE;
+    if (M < 0 || N < 0 || K < 0 || K % 32 != 0 || ldd < N) return NV4_ERR_SHAPE;
+    if (M == 0 || N == 0) return NV4_OK;
+    if (K == 0) return NV4_ERR_SHAPE;
+    if (qa == nullptr || sfa_mma == nullptr || qb == nullptr || sfb_mma == nullptr || out == nullptr) return NV4_ERR_NULL;
+    if (!aligned16(qa) || !aligned16(qb) || !aligned16(sfa_mma) || !aligned16(sfb_mma) || !aligned16(out)) return NV4_ERR_ALIGN;
+    if (M >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 31 ||
+        ((M + 255) / 256) * ((N + 255) / 256) >= (int64_t)1 << 31)
+        return NV4_ERR_LIMIT;
+    return from_cuda(launch_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, M, N, K, (int)out_dt, out, ldd, d_flags,
+                                       (cudaStream_t)stream));
+}
+
 // ------------------------------------------------------------------ products on FP4 weights
 nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                             const uint8_t* scales, const float* d_s2, int64_t N, nv4_dtype out_dt, void* out,

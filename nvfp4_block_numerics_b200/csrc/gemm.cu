@@ -40,22 +40,23 @@
 // next to the scale buffers): the tensor pipe idles while the epilogue reads it.
 //
 // When M and N are multiples of 256 the product runs on CTA pairs instead (the kernel
-// gemm_nvfp4_pair_kernel below: 256 x 256 tiles, the 2-SM MMA): 8192^3 +2%, 16384 x 16384 x
+// gemm_pair_kernel below: 256 x 256 tiles, the 2-SM MMA): 8192^3 +2%, 16384 x 16384 x
 // 2048 +7%.  Its cross-CTA hand-offs use plain (CTA-scope) mbarrier waits and remote
 // arrives: with cluster-scope acquire/release on them the same kernel ran 40% slower.
 // Every mbarrier wait is bounded (kWaitLimitNs); on expiry the kernel sets
 // NV4_FLAG_TIMEOUT, every role stops, the stores are skipped, copies in flight are
 // drained and the tensor memory is released.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "nv4_async.cuh"
 #include "nv4_common.cuh"
 #include "nv4_internal.h"
+#include "nv4_tcgen05.cuh"
+#include "nv4_tensormap.h"
 
 namespace nv4 {
 
 namespace gemm {
+
+using namespace tc;
 
 constexpr int kBM = 128;
 constexpr int kBK = 256;                          // FP4 elements per stage (128 bytes per row)
@@ -106,105 +107,9 @@ struct Params {
     uint32_t n_tiles, k_stages, kt4;              // kt4 = K / 64: scale atoms per 128-row tile
     uint32_t tiles;                               // output tiles in all
     uint32_t* d_flags;
+    uint32_t M, N, mt, nt;                        // MXFP4: sizes, 128-row atom tiles of A and of B
+    uint32_t vec;                                 // MXFP4: ldd keeps 16-byte alignment
 };
-
-// ---------------------------------------------------------------- PTX helpers
-// Shared-memory matrix descriptor (Blackwell format): start address, leading and
-// stride byte offsets in 16-byte units, descriptor version 1 (bits 46-47) and the
-// layout/swizzle mode in bits 61-63 (0 none, 2 = 128-byte swizzle).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lbo & 0x3FFFu) << 16) |
-           ((uint64_t)(sbo & 0x3FFFu) << 32) | (1ull << 46) | ((uint64_t)layout << 61);
-}
-
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols)
-{
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-// Writes n consecutive 32-bit tensor-memory columns of this warp's 32 lanes (one register
-// per column and lane); the caller waits with tmem_st_wait before handing them on.
-template <int n>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[n]);
-
-template <>
-__device__ __forceinline__ void tmem_st<16>(uint32_t taddr, const uint32_t (&v)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                   "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-                   "r"(v[15])
-                 : "memory");
-}
-
-template <>
-__device__ __forceinline__ void tmem_st<32>(uint32_t taddr, const uint32_t (&v)[32])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                   "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-                   "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
-                   "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
-                   "r"(v[31])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t"
-                 "}"
-                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-                 : "memory");
-}
-
-// Arrives on mbar once every tcgen05 operation issued so far by this thread completes.
-__device__ __forceinline__ void tc_commit(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-// 32 consecutive FP32 accumulator columns of this warp's 32 lanes (one row per thread).
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32])
-{
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-}  // namespace gemm
-
-namespace gemm {
 
 template <int kBN, int kOut>   // tile width 128 | 256; output 0 bf16, 2 fp32
 __global__ void __launch_bounds__(kThreads, 1)
@@ -296,7 +201,7 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
                     const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.b[s]);
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
-                        mma_fp4(tmem, smem_desc(a0 + 32u * j, 1u, 64u, 2u), smem_desc(b0 + 32u * j, 1u, 64u, 2u),
+                        mma_fp4<false, false>(tmem, smem_desc(a0 + 32u * j, 1u, 64u, 2u), smem_desc(b0 + 32u * j, 1u, 64u, 2u),
                                 C::kIdesc, ta + 4u * j, tb + nb * j, (ks | j) != 0u ? 1u : 0u);
                     tc_commit(&sm.empty[s]);                       // frees the stage when these MMAs finish
                     tc_commit(&sm.sf_free[b]);                     // and the scale buffer
@@ -476,48 +381,17 @@ struct Smem2 {
     uint32_t issued, consumed;
 };
 
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols)
-{
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-__device__ __forceinline__ void mma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t"
-                 "}"
-                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-                 : "memory");
-}
-
-// Arrives on the barrier at bar's offset in both CTAs of the pair once every tcgen05
-// operation issued so far by this thread completes.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(smem_u32(bar)), "h"((uint16_t)3u)
-                 : "memory");
-}
-
-template <int kOut>
+template <bool kMx, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
-gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
+gemm_pair_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<256>;
     constexpr int kStages = kStages2;
-    constexpr uint32_t kTx = 2u * 128u * 128u + 4u * 512u + 8u * 512u;
-    // instruction descriptor: as Cfg<256>::kIdesc with M = 256 (the pair)
-    constexpr uint32_t kIdesc2 = (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+    constexpr uint32_t kAtoms = kMx ? 2u : 4u;                     // scale atoms per 128 rows and stage
+    constexpr uint32_t kTx = 2u * 128u * 128u + 3u * kAtoms * 512u;
+    // instruction descriptor: as Cfg<256>::kIdesc with M = 256 (the pair); E8M0 scales: bit 23
+    constexpr uint32_t kIdesc2 = (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 3) << 17) | (kMx ? 1u << 23 : 0u) |
+                                 ((uint32_t)(256 >> 4) << 24);
     extern __shared__ uint8_t smem_raw[];
     Smem2& sm = *reinterpret_cast<Smem2*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -566,11 +440,26 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
                     mbar_arrive_expect_tx(&sm.full[s], kTx);
                     tma_load_2d(sm.a[s], &p.map_a, &sm.full[s], (int)(ks * 128u), (int)(mrow * 128u));
                     tma_load_2d(sm.b[s], &p.map_b, &sm.full[s], (int)(ks * 128u), (int)(nrow * 128u));
-                    bulk_load(sm.sfa[s], p.sfa + ((size_t)mrow * p.kt4 + 4u * ks) * 512u, 2048u, &sm.full[s]);
+                    if constexpr (kMx) {
+                        // 2 atoms of 128 K-elements; past an odd end the last one again (its codes
+                        // are zeros there), past the last rows the last row tile (rows not stored)
+                        const uint32_t a1 = min(2u * ks + 1u, p.kt4 - 1u);
+                        const uint8_t* fa = p.sfa + (size_t)min(mrow, p.mt - 1u) * p.kt4 * 512u;
+                        bulk_load(sm.sfa[s], fa + 2u * ks * 512u, 512u, &sm.full[s]);
+                        bulk_load(sm.sfa[s] + 512u, fa + a1 * 512u, 512u, &sm.full[s]);
 #pragma unroll
-                    for (uint32_t h = 0; h < 2u; ++h)
-                        bulk_load(sm.sfb[s] + 2048u * h, p.sfb + ((size_t)(2u * n_tile + h) * p.kt4 + 4u * ks) * 512u,
-                                  2048u, &sm.full[s]);
+                        for (uint32_t h = 0; h < 2u; ++h) {
+                            const uint8_t* fb = p.sfb + (size_t)min(2u * n_tile + h, p.nt - 1u) * p.kt4 * 512u;
+                            bulk_load(sm.sfb[s] + 2048u * h, fb + 2u * ks * 512u, 512u, &sm.full[s]);
+                            bulk_load(sm.sfb[s] + 2048u * h + 512u, fb + a1 * 512u, 512u, &sm.full[s]);
+                        }
+                    } else {
+                        bulk_load(sm.sfa[s], p.sfa + ((size_t)mrow * p.kt4 + 4u * ks) * 512u, 2048u, &sm.full[s]);
+#pragma unroll
+                        for (uint32_t h = 0; h < 2u; ++h)
+                            bulk_load(sm.sfb[s] + 2048u * h, p.sfb + ((size_t)(2u * n_tile + h) * p.kt4 + 4u * ks) * 512u,
+                                      2048u, &sm.full[s]);
+                    }
                 }
             }
             sm.issued = g;
@@ -596,9 +485,13 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
                     const uint32_t ta = tmem + 256u + C::kSfCols * b, tb = ta + 16u;
                     const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.b[s]);
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j)
-                        mma_fp4_pair(tmem, smem_desc(a0 + 32u * j, 1u, 64u, 2u), smem_desc(b0 + 32u * j, 1u, 64u, 2u),
-                                     kIdesc2, ta + 4u * j, tb + 8u * j, (ks | j) != 0u ? 1u : 0u);
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        // MXFP4: an atom's words serve two steps, the second from byte 2 on
+                        const uint32_t at = kMx ? j >> 1 : j, id = kMx ? 2u * (j & 1u) : 0u;
+                        mma_fp4<true, kMx>(tmem, smem_desc(a0 + 32u * j, 1u, 64u, 2u),
+                                           smem_desc(b0 + 32u * j, 1u, 64u, 2u), kIdesc2 | (id << 29) | (id << 4),
+                                           ta + 4u * at, tb + 8u * at, (ks | j) != 0u ? 1u : 0u);
+                    }
                     tc_commit_pair(&sm.empty[s]);
                     tc_commit_pair(&sm.sf_free[b]);
                 }
@@ -640,9 +533,9 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
                     break;
                 }
                 tc_fence_after();
-                uint32_t va[16], vb[32];
+                uint32_t va[4 * kAtoms], vb[8 * kAtoms];
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j) {
+                for (uint32_t j = 0; j < kAtoms; ++j) {
                     const uint4 x = *reinterpret_cast<const uint4*>(sm.sfa[s] + 512u * j + 16u * lane);
                     va[4 * j] = x.x; va[4 * j + 1] = x.y; va[4 * j + 2] = x.z; va[4 * j + 3] = x.w;
 #pragma unroll
@@ -653,8 +546,8 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
                     }
                 }
                 const uint32_t ta = tmem + lanes + 256u + C::kSfCols * b;
-                tmem_st<16>(ta, va);
-                tmem_st<32>(ta + 16u, vb);
+                tmem_st<4 * kAtoms>(ta, va);
+                tmem_st<8 * kAtoms>(ta + 16u, vb);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -669,7 +562,7 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
         // ---- epilogue warps 0-3 and 10-13, as in the single-CTA kernel; rows 128 * rank + ...
         const uint32_t q = (uint32_t)warp & 3u, h = warp >= 10 ? 1u : 0u;
         uint8_t* st = sm.stg[q + 4u * h];
-        const float alpha = __fmul_rn(*p.d_s2a, *p.d_s2b);
+        const float alpha = kMx ? 1.0f : __fmul_rn(*p.d_s2a, *p.d_s2b);
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
@@ -698,9 +591,18 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
                     tmem_ld32(taddr + (uint32_t)(32 * cb), v);
                     float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (row0 + lane) * p.ldd + col0 + 32 * cb);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = 0; k < 8; ++k) {
+                        const int64_t col = col0 + 32 * cb + 4 * k;
+                        if (kMx && (row0 + lane >= p.M || col + 4 > p.N || p.vec == 0u)) {
+                            if (row0 + lane < p.M)
+                                for (int i2 = 0; i2 < 4; ++i2)
+                                    if (col + i2 < p.N)
+                                        static_cast<float*>(p.out)[(row0 + lane) * p.ldd + col + i2] = v[4 * k + i2];
+                            continue;
+                        }
                         o[k] = make_float4(__fmul_rn(v[4 * k], alpha), __fmul_rn(v[4 * k + 1], alpha),
                                            __fmul_rn(v[4 * k + 2], alpha), __fmul_rn(v[4 * k + 3], alpha));
+                    }
                 }
                 release();
             } else {
@@ -729,6 +631,18 @@ gemm_nvfp4_pair_kernel(const __grid_constant__ Params p)
                     for (int k = 0; k < 2; ++k) {
                         const int rr = pr + 16 * k;
                         const uint4 x = *reinterpret_cast<const uint4*>(st + 32 * rr + 16 * (pc ^ ((rr >> 2) & 1)));
+                        const int64_t col = col0 + 16 * c16 + 8 * pc;
+                        if (kMx && (row0 + rr >= p.M || col + 8 > p.N || p.vec == 0u)) {
+                            if (row0 + rr < p.M) {
+                                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int i2 = 0; i2 < 8; ++i2)
+                                    if (col + i2 < p.N)
+                                        static_cast<uint16_t*>(p.out)[(row0 + rr) * p.ldd + col + i2] =
+                                            (uint16_t)(xw[i2 >> 1] >> (16 * (i2 & 1)));
+                            }
+                            continue;
+                        }
                         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row0 + rr) * p.ldd + col0 + 16 * c16 +
                                                   8 * pc) = x;
                     }
@@ -779,30 +693,47 @@ mma_scale_layout_kernel(const uint8_t* __restrict__ sc, uint32_t rows, uint32_t 
     }
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (fn == nullptr) {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
+}  // namespace gemm
 
-static bool code_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t K, uint32_t box_rows)
+namespace gemm {
+
+// Persistent launch of the pair kernel: as many pairs as can be resident at once.
+template <bool kMx, int kOut>
+static cudaError_t run_pair(const Params& p, int dev, cudaStream_t s)
 {
-    auto enc = encoder();
-    if (enc == nullptr) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t box[2] = {128u, box_rows};
-    const cuuint32_t es[2] = {1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    static bool attr_set[64] = {};
+    static int resident[64] = {};
+    const size_t smem = sizeof(Smem2) + 1024;
+    auto kern = gemm_pair_kernel<kMx, kOut>;
+    const bool known = dev >= 0 && dev < 64;
+    if (!known || !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        if (known) attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int pairs_cap = known ? resident[dev] : 0;
+    if (pairs_cap <= 0) {
+        cfg.gridDim = dim3(2u * (uint32_t)(num_sms() / 2), 1, 1);
+        if (cudaOccupancyMaxActiveClusters(&pairs_cap, kern, &cfg) != cudaSuccess || pairs_cap <= 0) {
+            (void)cudaGetLastError();
+            pairs_cap = num_sms() / 2;
+        }
+        if (known) resident[dev] = pairs_cap;
+    }
+    cfg.gridDim = dim3(2u * (p.tiles < (uint32_t)pairs_cap ? p.tiles : (uint32_t)pairs_cap), 1, 1);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace gemm
@@ -829,8 +760,8 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa, const float
                               void* out, int64_t ldd, uint32_t* d_flags, cudaStream_t s)
 {
     using namespace gemm;
-    Params p;
-    static bool attr_set[6][64] = {};
+    Params p = {};
+    static bool attr_set[4][64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -849,40 +780,7 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa, const float
         p.kt4 = (uint32_t)(K / 64);
         p.tiles = (uint32_t)((M / 256) * (N / 256));
         p.d_flags = d_flags;
-        const size_t smem = sizeof(Smem2) + 1024;
-        auto kern = o ? gemm_nvfp4_pair_kernel<2> : gemm_nvfp4_pair_kernel<0>;
-        if (dev < 0 || dev >= 64 || !attr_set[4 + o][dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) attr_set[4 + o][dev] = true;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        // persistent: as many pairs as can be resident at once (once per device and output type)
-        static int resident[2][64] = {};
-        int pairs_cap = dev >= 0 && dev < 64 ? resident[o][dev] : 0;
-        if (pairs_cap <= 0) {
-            cfg.gridDim = dim3(2u * (uint32_t)(num_sms() / 2), 1, 1);
-            if (cudaOccupancyMaxActiveClusters(&pairs_cap, kern, &cfg) != cudaSuccess || pairs_cap <= 0) {
-                (void)cudaGetLastError();
-                pairs_cap = num_sms() / 2;
-            }
-            if (dev >= 0 && dev < 64) resident[o][dev] = pairs_cap;
-        }
-        const uint32_t npairs = p.tiles < (uint32_t)pairs_cap ? p.tiles : (uint32_t)pairs_cap;
-        cfg.gridDim = dim3(2u * npairs, 1, 1);
-        e = cudaLaunchKernelEx(&cfg, kern, p);
-        if (e != cudaSuccess) return e;
-        return cudaGetLastError();
+        return o ? run_pair<false, 2>(p, dev, s) : run_pair<false, 0>(p, dev, s);
     }
     const bool wide = N % 256 == 0;
     const int bn = wide ? 256 : 128;
@@ -910,6 +808,33 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa, const float
     const unsigned grid = (unsigned)(p.tiles < (uint32_t)num_sms() ? p.tiles : (uint32_t)num_sms());
     kern<<<grid, kThreads, smem, s>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
+                              int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,
+                              cudaStream_t s)
+{
+    using namespace gemm;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Params p = {};
+    if (!code_map(&p.map_a, qa, M, K, 128u) || !code_map(&p.map_b, qb, N, K, 128u)) return cudaErrorInvalidValue;
+    p.sfa = sfa;
+    p.sfb = sfb;
+    p.out = out;
+    p.ldd = ldd;
+    p.n_tiles = (uint32_t)((N + 255) / 256);
+    p.k_stages = (uint32_t)((K + kBK - 1) / kBK);
+    p.kt4 = (uint32_t)((K + 127) / 128);
+    p.tiles = (uint32_t)((M + 255) / 256) * p.n_tiles;
+    p.d_flags = d_flags;
+    p.M = (uint32_t)M;
+    p.N = (uint32_t)N;
+    p.mt = (uint32_t)((M + 127) / 128);
+    p.nt = (uint32_t)((N + 127) / 128);
+    p.vec = ldd % (out_dt == 2 ? 4 : 8) == 0 ? 1u : 0u;
+    return out_dt == 2 ? run_pair<true, 2>(p, dev, s) : run_pair<true, 0>(p, dev, s);
 }
 
 }  // namespace nv4

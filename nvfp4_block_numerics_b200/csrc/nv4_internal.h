@@ -111,6 +111,11 @@ struct MoeExpertsArgs {
 cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_t ldx, const void* wr, int64_t E,
                              int top_k, int renorm, int32_t* ids, float* weights, uint32_t* d_flags, cudaStream_t s);
 cudaError_t launch_moe_experts(const MoeExpertsArgs& a, cudaStream_t s);
+cudaError_t launch_mxfp4_quant_mma(const void* x, int in_dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
+                                   uint8_t* sf, uint32_t* d_flags, cudaStream_t s);
+cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
+                              int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,
+                              cudaStream_t s);
 cudaError_t launch_dequant(const DequantTask* tasks, int n, int out_dt, cudaStream_t s);
 cudaError_t launch_hessian(const nv4_hessian_job* jobs, int n, uint32_t* d_flags, cudaStream_t s, int* bad_job);
 cudaError_t launch_sweep(const nv4_sweep_job* jobs, int n, int dt, uint32_t* d_flags, cudaStream_t s);

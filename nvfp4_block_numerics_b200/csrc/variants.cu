@@ -112,6 +112,52 @@ mxfp4_quant_kernel(const void* x, uint32_t rows, uint32_t halves_per_row, int64_
     if ((threadIdx.x & 31) == 0) flag_or(d_flags, flags);
 }
 
+// As mxfp4_quant_kernel, with the scales in the layout that the block-scaled MMA reads: 512-byte
+// atoms of 128 rows x 4 blocks.  The 8 lanes of 4 blocks (128 elements) put their four scale
+// bytes together by shuffles and store one word, so the scales need no second pass.  The row
+// and block padding of the atoms is written as zeros.
+template <int kIn>
+__global__ void __launch_bounds__(kVarThreads)
+mxfp4_quant_mma_kernel(const void* x, uint32_t rows, uint32_t cols, uint32_t kt, FastDiv div_h, int64_t ld,
+                       uint8_t* __restrict__ q, uint32_t* __restrict__ sf, uint32_t total,
+                       uint32_t* __restrict__ d_flags)
+{
+    const uint32_t lane = threadIdx.x & 31u, hpr = kt * 8u;       // half blocks per padded row
+    uint32_t flags = 0u;
+    // total = padded rows x hpr is a multiple of 32: every warp is whole
+    for (uint32_t h = blockIdx.x * kVarThreads + threadIdx.x; h < total; h += gridDim.x * kVarThreads) {
+        const uint32_t r = div_h.div(h), hh = h - r * hpr, k = 16u * hh;
+        const bool live = r < rows && k < cols;
+        float v[16];
+        uint32_t ab = 0u, code = 0u;
+        if (live) load16<kIn>(x, (int64_t)r * ld + k, v, ab);
+        ab = max(ab, __shfl_xor_sync(0xFFFFFFFFu, ab, 1));
+        if (live) {
+            uint32_t c0 = 0u, c1 = 0u;
+            if (ab >= 0x7F800000u) {
+                flags |= kFlagNonFinite;
+                code = 0xFFu;
+            } else {
+                const int e = ab == 0u ? -127 : max(floor_log2_bits(ab) - 2, -127);
+                code = (uint32_t)(e + 127);
+                const float inv = pow2f(-e);
+                float y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(v[i], inv);
+                c0 = cvt_e2m1x8(y);
+                c1 = cvt_e2m1x8(y + 8);
+            }
+            *reinterpret_cast<uint2*>(q + (int64_t)r * (cols / 2u) + 8u * hh) = make_uint2(c0, c1);
+        }
+        uint32_t w = code << (8u * ((lane >> 1) & 3u));
+        w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+        w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+        if ((lane & 7u) == 0u) sf[((r >> 7) * kt + (hh >> 3)) * 128u + (r & 31u) * 4u + ((r & 127u) >> 5)] = w;
+    }
+    flags = __reduce_or_sync(__activemask(), flags);
+    if ((threadIdx.x & 31) == 0) flag_or(d_flags, flags);
+}
+
 // One thread per 8 outputs: 4 code bytes, the block's E8M0 byte, 8 outputs.
 template <int kOut>
 __global__ void __launch_bounds__(kVarThreads)
@@ -408,6 +454,17 @@ cudaError_t launch_mxfp4_quant(const void* x, int in_dt, int64_t rows, int64_t c
         mxfp4_quant_kernel<0><<<g, kVarThreads, 0, s>>>(x, (uint32_t)rows, hpr, ld, FastDiv(hpr), q, e8m0, d_flags);
     else
         mxfp4_quant_kernel<2><<<g, kVarThreads, 0, s>>>(x, (uint32_t)rows, hpr, ld, FastDiv(hpr), q, e8m0, d_flags);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mxfp4_quant_mma(const void* x, int in_dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
+                                   uint8_t* sf, uint32_t* d_flags, cudaStream_t s)
+{
+    const uint32_t kt = (uint32_t)((cols + 127) / 128), total = (uint32_t)((rows + 127) / 128) * 128u * kt * 8u;
+    const uint32_t need = (total + kVarThreads - 1) / kVarThreads, cap = (uint32_t)num_sms() * 8u;
+    auto kern = in_dt == 0 ? mxfp4_quant_mma_kernel<0> : mxfp4_quant_mma_kernel<2>;
+    kern<<<need < cap ? need : cap, kVarThreads, 0, s>>>(x, (uint32_t)rows, (uint32_t)cols, kt, FastDiv(kt * 8u), ld, q,
+                                                        reinterpret_cast<uint32_t*>(sf), total, d_flags);
     return cudaGetLastError();
 }
 

@@ -412,6 +412,22 @@ def scales_to_mma_layout(sc: np.ndarray) -> np.ndarray:
     return out
 
 
+# ---------------------------------------------------------------- MXFP4 product
+def gemm_mxfp4(qa, ea, qb, eb):
+    """MXFP4 x MXFP4 product D[m, n] = sum_k A[m, k] B[n, k] in FP64, value = e2m1(code) *
+    2^(e8m0 - 127) with row-major scales [rows, K/32] ([FP4] sections 1.2 and 4.1).  Returns
+    (D, |A| |B|^T)."""
+    e2m1 = np.array([e2m1_value(c) for c in range(16)], np.float64)
+
+    def values(q, e):
+        nib = np.stack([q & 15, q >> 4], axis=-1).reshape(q.shape[0], -1)
+        s = np.where(e == 255, np.nan, np.ldexp(1.0, e.astype(np.int64) - 127))
+        return e2m1[nib] * np.repeat(s, 32, axis=1)
+
+    A, B = values(np.ascontiguousarray(qa), ea), values(np.ascontiguousarray(qb), eb)
+    return A @ B.T, np.abs(A) @ np.abs(B).T
+
+
 # ---------------------------------------------------------------- weight-only linear layer
 def linear_w4a16(x: np.ndarray, q: np.ndarray, sc: np.ndarray, s2: float):
     """y[t, n] = sum_k x[t, k] * e2m1(q[n, k]) * e4m3(sc[n, k/16]) * s2 in FP64 for 16-bit rows

@@ -95,3 +95,32 @@ def test_moe_oracle_small(orc):
     assert np.all(one(-1) == 0) and np.all(one(3) == 0)
     ids, w = orc.moe_route(np.array([[1.0, 0.0]]), np.array([[0.0, 1.0], [2.0, 0.0], [2.0, 0.0]]), 2)
     assert ids.tolist() == [[1, 2]] and np.allclose(w, 0.5)
+
+
+def test_mxfp4_product_refusals(L):
+    def quant(x=FAKE, dt=0, rows=4, cols=64, ld=64, q=FAKE, s=FAKE):
+        return L.nv4_mxfp4_quant_mma(x, dt, rows, cols, ld, q, s, None, None)
+
+    assert quant(dt=1) == 4 and quant(cols=48, ld=48) == 2 and quant(ld=32) == 2
+    assert quant(x=None) == 1 and quant(s=None) == 1 and quant(s=FAKE + 8) == 3 and quant(ld=68) == 3
+    assert quant(rows=0) == 0 and quant(rows=1 << 30, cols=1 << 12, ld=1 << 12) == 6
+
+    def gemm(qa=FAKE, sa=FAKE, qb=FAKE, sb=FAKE, M=4, N=8, K=64, dt=0, out=FAKE, ldd=8):
+        return L.nv4_gemm_mxfp4(qa, sa, qb, sb, M, N, K, dt, out, ldd, None, None)
+
+    assert gemm(dt=1) == 4 and gemm(K=48) == 2 and gemm(ldd=7) == 2 and gemm(K=0) == 2 and gemm(M=-1) == 2
+    assert gemm(qa=None) == 1 and gemm(sb=None) == 1 and gemm(out=None) == 1
+    assert gemm(qb=FAKE + 8) == 3 and gemm(sa=FAKE + 4) == 3 and gemm(out=FAKE + 8) == 3
+    assert gemm(M=0) == 0 and gemm(N=0, ldd=0) == 0 and gemm(M=1 << 31) == 6
+    assert L.nv4_mxfp4_mma_scale_bytes(200, 288) == 256 * 12 and L.nv4_mxfp4_mma_scale_bytes(1, 32) == 512
+    assert L.nv4_mxfp4_mma_scale_bytes(4, 48) == 0 and L.nv4_mxfp4_mma_scale_bytes(0, 32) == 0
+
+
+def test_mxfp4_product_oracle_small(orc):
+    """Against the oracle's dequantizer, which is pinned to the format."""
+    rng = np.random.default_rng(3)
+    qa, qb = rng.integers(0, 256, (3, 32), dtype=np.uint8), rng.integers(0, 256, (5, 32), dtype=np.uint8)
+    ea, eb = rng.integers(100, 150, (3, 2), dtype=np.uint8), rng.integers(100, 150, (5, 2), dtype=np.uint8)
+    D, Dabs = orc.gemm_mxfp4(qa, ea, qb, eb)
+    A, B = (orc.mxfp4_dequant(q, e, "fp32").astype(np.float64) for q, e in ((qa, ea), (qb, eb)))
+    assert np.allclose(D, A @ B.T, rtol=1e-12) and np.allclose(Dabs, np.abs(A) @ np.abs(B).T, rtol=1e-12)
