@@ -526,7 +526,7 @@ NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int6
  * down     : codes [E, H, I/2], scales [E, H, I/16], d_s2 [E]; all contiguous.
  * ids      : int32 [T, top_k]; weights: float [T, top_k]; both contiguous.
  * out      : [T, H] of out_dt, leading dimension ldd >= H, 16-byte aligned base.
- * d_work   : nv4_moe_work_bytes(T, top_k, I) bytes, 16-byte aligned, not shared by calls that
+ * d_work   : nv4_moe_work_bytes(T, top_k, H, I) bytes, 16-byte aligned, not shared by calls that
  *            may run at the same time; nothing has to be in it and nothing is kept in it.
  * Limits (NV4_ERR_LIMIT beyond): T <= 64, T * top_k <= 2048, E <= 512, top_k <= min(32, E),
  * H, I <= 32768.  H and I multiples of 16 (NV4_ERR_SHAPE).  T == 0 is a no-op.
@@ -540,7 +540,7 @@ typedef struct {
 NV4_API nv4_status nv4_moe_route(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx,
                          const void* w_router, int64_t E, int top_k, int renormalize, int32_t* ids,
                          float* weights, uint32_t* d_flags, void* stream);
-NV4_API size_t nv4_moe_work_bytes(int64_t T, int top_k, int64_t I);
+NV4_API size_t nv4_moe_work_bytes(int64_t T, int top_k, int64_t H, int64_t I);
 NV4_API nv4_status nv4_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx,
                            const int32_t* ids, const float* weights, int top_k, int64_t E, int64_t I,
                            const nv4_expert_weights* gate, const nv4_expert_weights* up,

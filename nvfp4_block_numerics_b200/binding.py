@@ -107,7 +107,7 @@ _SIGS = {
     "nv4_mxfp4_quant_mma": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "nv4_gemm_mxfp4": (C.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _i64, _vp, _vp]),
     "nv4_moe_route": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _i64, C.c_int, C.c_int, _vp, _vp, _vp, _vp]),
-    "nv4_moe_work_bytes": (C.c_size_t, [_i64, C.c_int, _i64]),
+    "nv4_moe_work_bytes": (C.c_size_t, [_i64, C.c_int, _i64, _i64]),
     "nv4_moe_experts": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, C.c_int, _i64, _i64,
                                   C.POINTER(ExpertWeights), C.POINTER(ExpertWeights), C.POINTER(ExpertWeights), C.c_int,
                                   _vp, _i64, _vp, C.c_size_t, _vp, _vp]),
@@ -808,13 +808,13 @@ def _moe_shapes(x, gate, down, out, work, k: int):
     orows, ocols, ldd = _rowmajor(out, "out")
     if (orows, ocols) != (T, H):
         raise NV4Error("out must be [T, H]")
-    if not work.is_contiguous() or work.numel() * work.element_size() < nv4_moe_work_bytes(T, k, I):
-        raise NV4Error(f"work must be a contiguous tensor of at least {nv4_moe_work_bytes(T, k, I)} bytes")
+    if not work.is_contiguous() or work.numel() * work.element_size() < nv4_moe_work_bytes(T, k, H, I):
+        raise NV4Error(f"work must be a contiguous tensor of at least {nv4_moe_work_bytes(T, k, H, I)} bytes")
     return T, H, ldx, E, I, max(ldd, H) if T <= 1 else ldd
 
 
-def nv4_moe_work_bytes(T: int, top_k: int, I: int) -> int:
-    return int(lib().nv4_moe_work_bytes(T, top_k, I))
+def nv4_moe_work_bytes(T: int, top_k: int, H: int, I: int) -> int:
+    return int(lib().nv4_moe_work_bytes(T, top_k, H, I))
 
 
 def nv4_moe_route(x, w_router, ids, weights, renormalize=True, d_flags=None, stream=None):
@@ -828,7 +828,7 @@ def nv4_moe_route(x, w_router, ids, weights, renormalize=True, d_flags=None, str
 
 def nv4_moe_experts(x, ids, weights, gate, up, down, out, work, d_flags=None, stream=None):
     """out[t] = sum_j weights[t, j] * down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j]; gate, up and
-    down: (codes, scales, s2) of every expert's matrix; work: nv4_moe_work_bytes(T, top_k, I) bytes."""
+    down: (codes, scales, s2) of every expert's matrix; work: nv4_moe_work_bytes(T, top_k, H, I) bytes."""
     _here(x, ids, weights, *gate, *up, *down, out, work, d_flags)
     k = _routing(ids, weights, x.shape[0])
     T, H, ldx, E, I, ldd = _moe_shapes(x, gate, down, out, work, k)
@@ -865,7 +865,7 @@ def moe_route(x, w_router, top_k: int, renormalize=True, d_flags=None, stream=No
 def moe_experts(x, ids, weights, gate, up, down, dtype=None, d_flags=None, stream=None):
     """x [T, H] through the chosen experts -> [T, H] of dtype (default: x's)."""
     out = _new(tuple(x.shape), dtype or x.dtype, x, stream)
-    work = _new((ids.numel() * gate[0].shape[1],), torch.float32, x, stream)
+    work = _new((nv4_moe_work_bytes(x.shape[0], ids.shape[1], x.shape[1], gate[0].shape[1]),), torch.uint8, x, stream)
     nv4_moe_experts(x, ids, weights, gate, up, down, out, work, d_flags, stream)
     return out
 
@@ -876,7 +876,7 @@ def moe_layer(x, w_router, gate, up, down, top_k: int, renormalize=True, dtype=N
     out = _new(tuple(x.shape), dtype or x.dtype, x, stream)
     ids = _new((T, top_k), torch.int32, x, stream)
     weights = _new((T, top_k), torch.float32, x, stream)
-    work = _new((T * top_k * gate[0].shape[1],), torch.float32, x, stream)
+    work = _new((nv4_moe_work_bytes(T, top_k, x.shape[1], gate[0].shape[1]),), torch.uint8, x, stream)
     nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize, d_flags, stream)
     return out, ids, weights
 

@@ -598,19 +598,16 @@ static nv4_status check_moe_experts(int64_t T, int64_t H, int64_t I, const nv4_e
     for (int i = 0; i < 3; ++i)
         if (!aligned16(w[i]->q) || !aligned16(w[i]->scales) || !aligned4(w[i]->d_s2)) return NV4_ERR_ALIGN;
     if (!aligned16(out) || !aligned16(work) || !aligned4(ids) || !aligned4(weights)) return NV4_ERR_ALIGN;
-    if (work_bytes < nv4_moe_work_bytes(T, top_k, I)) return NV4_ERR_LIMIT;
+    if (work_bytes < moe_work_bytes(T, top_k, H, I)) return NV4_ERR_LIMIT;
     return NV4_OK;
 }
 
-static nv4_status run_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
-                                  const float* weights, int top_k, int64_t E, int64_t I,
-                                  const nv4_expert_weights* const w[3], nv4_dtype out_dt, void* out, int64_t ldd,
-                                  void* work, void* stream)
+static MoeExpertsArgs moe_args(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
+                               const float* weights, int top_k, int64_t E, int64_t I,
+                               const nv4_expert_weights* const w[3], nv4_dtype out_dt, void* out, int64_t ldd, void* work)
 {
-    const MoeExpertsArgs a{x, (int)dt, (int)out_dt, T, top_k, E, H, I, ldx, ldd, ids, weights, w[0]->q, w[0]->scales,
-                           w[1]->q, w[1]->scales, w[2]->q, w[2]->scales, w[0]->d_s2, w[1]->d_s2, w[2]->d_s2,
-                           static_cast<float*>(work), out};
-    return from_cuda(launch_moe_experts(a, (cudaStream_t)stream));
+    return MoeExpertsArgs{x, (int)dt, (int)out_dt, T, top_k, E, H, I, ldx, ldd, ids, weights, w[0]->q, w[0]->scales,
+                          w[1]->q, w[1]->scales, w[2]->q, w[2]->scales, w[0]->d_s2, w[1]->d_s2, w[2]->d_s2, work, out};
 }
 
 nv4_status nv4_moe_route(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const void* w_router,
@@ -622,13 +619,15 @@ nv4_status nv4_moe_route(const void* x, nv4_dtype dt, int64_t T, int64_t H, int6
     if (w_router == nullptr || ids == nullptr || weights == nullptr) return NV4_ERR_NULL;
     if (!aligned16(w_router) || !aligned4(ids) || !aligned4(weights)) return NV4_ERR_ALIGN;
     return from_cuda(launch_moe_route(x, (int)dt, T, H, ldx, w_router, E, top_k, renormalize != 0, ids, weights,
-                                      d_flags, (cudaStream_t)stream));
+                                      nullptr, d_flags, (cudaStream_t)stream));
 }
 
-size_t nv4_moe_work_bytes(int64_t T, int top_k, int64_t I)
+size_t nv4_moe_work_bytes(int64_t T, int top_k, int64_t H, int64_t I)
 {
-    if (T <= 0 || top_k <= 0 || I <= 0) return 0;
-    return (size_t)T * (size_t)top_k * (size_t)I * sizeof(float);
+    if (T <= 0 || top_k <= 0 || H <= 0 || I <= 0 || T > kMaxMoeTokens || top_k > kMaxMoeTopK || H > kMaxMoeWidth ||
+        I > kMaxMoeWidth)
+        return 0;
+    return moe_work_bytes(T, top_k, H, I);
 }
 
 nv4_status nv4_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
@@ -641,7 +640,8 @@ nv4_status nv4_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, in
     nv4_status st = check_moe_rows(x, dt, T, H, ldx, E, top_k);
     if (st == NV4_OK) st = check_moe_experts(T, H, I, w, ids, weights, top_k, out_dt, out, ldd, d_work, work_bytes);
     if (st != NV4_OK || T == 0) return st;
-    return run_moe_experts(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work, stream);
+    return from_cuda(launch_moe_experts(
+        moe_args(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work), false, (cudaStream_t)stream));
 }
 
 nv4_status nv4_moe_layer(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const void* w_router,
@@ -654,9 +654,13 @@ nv4_status nv4_moe_layer(const void* x, nv4_dtype dt, int64_t T, int64_t H, int6
     nv4_status st = check_moe_rows(x, dt, T, H, ldx, E, top_k);
     if (st == NV4_OK) st = check_moe_experts(T, H, I, w, ids, weights, top_k, out_dt, out, ldd, d_work, work_bytes);
     if (st != NV4_OK || T == 0) return st;
-    st = nv4_moe_route(x, dt, T, H, ldx, w_router, E, top_k, renormalize, ids, weights, d_flags, stream);
+    if (w_router == nullptr) return NV4_ERR_NULL;
+    if (!aligned16(w_router)) return NV4_ERR_ALIGN;
+    const MoeExpertsArgs a = moe_args(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work);
+    st = from_cuda(launch_moe_route(x, (int)dt, T, H, ldx, w_router, E, top_k, renormalize != 0, ids, weights, &a, d_flags,
+                                    (cudaStream_t)stream));
     if (st != NV4_OK) return st;
-    return run_moe_experts(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work, stream);
+    return from_cuda(launch_moe_experts(a, true, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------------------ format variants

@@ -7,22 +7,25 @@
 //            (ties: the lower index); weight = p, or p / sum of the chosen p
 //   experts  h = silu(gate_e x) * (up_e x);  y[t] = sum_j weight[t, j] * down_e h
 //
-// Three launches.  moe_route_kernel: one 8-CTA cluster per few tokens.  The products of 16-bit
-// values are exact in FP32 and are summed in FP64, so that the choice of experts is that of the
-// exact logits whatever the summation order.  moe_up_kernel and moe_down_kernel: one CTA per SM,
-// the product of nv4_w4.cuh on the experts that some token chose.  The bound is reading those
-// experts' weights once from HBM, so both kernels split the rows of all chosen experts evenly
-// over the SMs, to one row.
-//   * up: the flat list (expert, i) of gate / up row pairs is cut into one contiguous range per
-//     CTA, walked in tiles of 8 pairs: MMA rows 0-7 are gate rows, 8-15 the same up rows, so
-//     both halves of an h meet in one thread.  h goes to the workspace in FP32.
-//   * down: a CTA owns a range of output rows for all tokens and all chosen experts, so the sum
-//     over a token's experts needs no other CTA and is in a fixed order.  h is scaled per
-//     (token, expert) by a power of two and rounded to FP16 (11 bits: a relative error of 2^-11,
-//     an eighth of the BF16 output's own rounding); its scale, the expert's scale_2 and the
-//     routing weight are applied in FP32 to the accumulated product.
+// Four launches, each a programmatic dependent of the one before: its CTAs start, and do what
+// does not depend on it, while the last CTAs in front finish.
+//   * moe_route_kernel: a 16-CTA cluster per one to four tokens.  The products of 16-bit values
+//     are exact in FP32 and are summed in FP64, so that the choice of experts is that of the
+//     exact logits whatever the summation order.  It also converts BF16 token rows to FP16, each
+//     with a power of two of its own (moe_rows_kernel does where the experts are given).
+//   * moe_up_kernel, one CTA per SM: the flat list (expert, i) of gate / up row pairs of the
+//     chosen experts is cut into one contiguous range per CTA, walked in tiles of 8 pairs: MMA
+//     rows 0-7 are gate rows, 8-15 the same up rows, so both halves of an h meet in one thread.
+//     h goes to the workspace in FP32.
+//   * moe_hidden_kernel, one CTA per (expert, token) row of h: scales it by a power of two and
+//     rounds it to FP16 (11 bits: a relative error of 2^-11, an eighth of the BF16 output's own).
+//   * moe_down_kernel, one CTA per SM: a CTA owns a range of output rows for all tokens and all
+//     chosen experts, so the sum over a token's experts needs no other CTA and is in a fixed
+//     order.  The row's scale, the expert's scale_2 and the routing weight are applied in FP32.
+// The bound is reading the chosen experts' weights once from HBM; both products (nv4_w4.cuh) split
+// their rows evenly over the SMs, to one row, and read the token rows through L1.  An expert with
+// more than 8 tokens is multiplied in passes of 8.
 #include <cfloat>
-#include <type_traits>
 
 #include "nv4_async.cuh"
 #include "nv4_internal.h"
@@ -32,17 +35,98 @@ namespace nv4 {
 
 namespace moe {
 
-using w4::Frag;
 using w4::kChunk;
 using w4::kThreads;
 using w4::kWarps;
 
-constexpr uint32_t kPass = 24;                    // tokens of one expert multiplied at once
+constexpr uint32_t kPass = 8;                     // tokens of one expert multiplied at once
+
+// ---------------------------------------------------------------- token rows
+// The workspace: x as FP16 [T][H], what undoes each row's scaling (negative: the row is not held
+// by FP16, see w4::stage_tokens), h in FP32 [rows][I], h as FP16 [rows][I], its scales.
+struct Work {
+    uint16_t* x16;
+    float* xd;
+    float* h;
+    uint16_t* h16;
+    float* hd;
+};
+
+__host__ __device__ inline size_t align256(size_t n) { return (n + 255u) & ~(size_t)255u; }
+
+__host__ inline Work work_of(void* w, size_t T, size_t k, size_t H, size_t I, size_t* bytes)
+{
+    uint8_t* b = static_cast<uint8_t*>(w);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        uint8_t* r = b + at;
+        at += align256(n);
+        return r;
+    };
+    Work o;
+    o.x16 = reinterpret_cast<uint16_t*>(take(T * H * 2u));
+    o.xd = reinterpret_cast<float*>(take(T * 4u));
+    o.h = reinterpret_cast<float*>(take(T * k * I * 4u));
+    o.h16 = reinterpret_cast<uint16_t*>(take(T * k * I * 2u));
+    o.hd = reinterpret_cast<float*>(take(T * k * 4u));
+    *bytes = at;
+    return o;
+}
+
+// The CTA's threads convert one BF16 row to FP16 with a power of two of its own.
+__device__ __forceinline__ void convert_row(const uint16_t* x, uint32_t H, uint16_t* out, float* descale, uint32_t* red)
+{
+    const uint32_t tid = threadIdx.x, n = blockDim.x, warp = tid >> 5, lane = tid & 31u;
+    uint32_t hi = 0u, lo = 0xFFFFFFFFu;
+    for (uint32_t k = 8u * tid; k < H; k += 8u * n) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+        const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hi = __vmaxu2(hi, w[j]);
+            lo = __vminu2(lo, __vsub2(w[j], 0x00010001u));        // zero becomes 0xFFFF
+        }
+    }
+    hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16));
+    lo = __reduce_min_sync(0xFFFFFFFFu, min(lo & 0xFFFFu, lo >> 16));
+    if (lane == 0u) {
+        red[warp] = hi;
+        red[32u + warp] = lo;
+    }
+    __syncthreads();
+    for (uint32_t w = 0; w < n / 32u; ++w) {
+        hi = max(hi, red[w]);
+        lo = min(lo, red[32u + w]);
+    }
+    const int e1 = (int)(hi >> 7), e0 = (int)((lo + 1u) >> 7);
+    const bool wide = hi != 0u && (e1 == 255 || e0 == 0 || e1 - e0 > 31 || e1 < 20);
+    const float f = hi == 0u || wide ? 1.0f : w4::exp_field(268 - e1);
+    if (tid == 0u) *descale = wide ? -1.0f : hi == 0u ? 1.0f : w4::exp_field(e1 - 14);
+    for (uint32_t k = 8u * tid; k < H; k += 8u * n) {
+        uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                : "=r"(w[j])
+                : "f"(__fmul_rn(bf16_hi(w[j]), f)), "f"(__fmul_rn(bf16_lo(w[j]), f)));
+        *reinterpret_cast<uint4*>(out + k) = v;
+    }
+}
+
+__global__ void __launch_bounds__(512) moe_rows_kernel(const void* x, int64_t ldx, uint32_t H, Work w)
+{
+    __shared__ uint32_t red[64];
+    w4::pdl_launch();
+    convert_row(static_cast<const uint16_t*>(x) + (int64_t)blockIdx.x * ldx, H, w.x16 + (size_t)blockIdx.x * H,
+                w.xd + blockIdx.x, red);
+}
 
 // ---------------------------------------------------------------- router
-constexpr int kRouteThreads = 256;
-constexpr uint32_t kRouteCtas = 8;                // one cluster
+constexpr int kRouteThreads = 512;
+constexpr uint32_t kRouteCtas = 16;               // one cluster
 constexpr uint32_t kRouteTokens = 4;              // tokens per cluster
+constexpr uint32_t kRouteParts = 4;               // warps that share a logit, each a quarter of H
 
 struct RouteParams {
     const void* x;
@@ -52,6 +136,7 @@ struct RouteParams {
     float* weights;
     uint32_t T, H, E, k, renorm;
     uint32_t* d_flags;
+    Work work;                                    // x16: null, or where to put the rows as FP16
 };
 
 template <int kDt>
@@ -69,101 +154,109 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])
     }
 }
 
-template <int kDt>
-__global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThreads)
-moe_route_kernel(const __grid_constant__ RouteParams p)
+// kTok: tokens of the cluster (1, or up to kRouteTokens).  CTA i of the cluster collects the
+// logits of token i and chooses: an expert's place is the number of experts that rank above it,
+// so no round waits for the one before.
+template <int kDt, int kTok>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_constant__ RouteParams p)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    double* logits = reinterpret_cast<double*>(smem);              // [kRouteTokens][E], in the cluster's rank 0
-    const uint32_t rank = cluster_ctarank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    __shared__ double part[kMaxMoeExperts][kRouteParts];
+    __shared__ double logit[kMaxMoeExperts];
+    __shared__ double chosen[kMaxMoeTopK];
+    __shared__ double sums[kRouteThreads / 32];
+    const uint32_t tid = threadIdx.x, rank = cluster_ctarank(), warp = tid >> 5, lane = tid & 31u;
     constexpr uint32_t kRW = kRouteThreads / 32;
-    const uint32_t t0 = (blockIdx.x / kRouteCtas) * kRouteTokens, nt = min(kRouteTokens, p.T - t0);
-    const uint16_t* x = static_cast<const uint16_t*>(p.x);
+    const uint32_t t0 = (blockIdx.x / kRouteCtas) * kTok, nt = min((uint32_t)kTok, p.T - t0);
+    const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)t0 * p.ldx;
     const uint16_t* wr = static_cast<const uint16_t*>(p.wr);
-    uint32_t flags = 0u;
-    cluster_sync();                                                // rank 0 runs: its shared memory can be written
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");              // this CTA runs
+    w4::pdl_launch();
 
-    for (uint32_t e = rank * kRW + warp; e < p.E; e += kRouteCtas * kRW) {
-        double s[kRouteTokens];
+    // unit (expert, quarter): vectors of 8 values lane + 32 * quarter, + 128, ...
+    bool waited = false;
+    for (uint32_t u = rank * kRW + warp; u < p.E * kRouteParts; u += kRouteCtas * kRW) {
+        const uint32_t e = u / kRouteParts, q = u % kRouteParts;
+        double s[kTok][4];
 #pragma unroll
-        for (uint32_t i = 0; i < kRouteTokens; ++i) s[i] = 0.0;
-        for (uint32_t h = 8u * lane; h < p.H; h += 256u) {
+        for (int i = 0; i < kTok; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0;
+#pragma unroll 4
+        for (uint32_t h = 8u * (lane + 32u * q); h < p.H; h += 8u * 32u * kRouteParts) {
             float w[8];
             unpack8<kDt>(__ldg(reinterpret_cast<const uint4*>(wr + (size_t)e * p.H + h)), w);
 #pragma unroll
-            for (uint32_t i = 0; i < kRouteTokens; ++i) {
-                if (i >= nt) break;
-                float v[8];
-                unpack8<kDt>(__ldg(reinterpret_cast<const uint4*>(x + (int64_t)(t0 + i) * p.ldx + h)), v);
+            for (int i = 0; i < kTok; ++i) {
+                if ((uint32_t)i < nt) {
+                    float v[8];
+                    unpack8<kDt>(__ldg(reinterpret_cast<const uint4*>(x + (int64_t)i * p.ldx + h)), v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[i] = fma((double)v[j], (double)w[j], s[i]);
+                    for (int j = 0; j < 8; ++j) s[i][j & 3] += (double)__fmul_rn(v[j], w[j]);   // exact product
+                }
             }
         }
+        if (!waited) {                                             // the other CTAs run: write to them
+            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            waited = true;
+        }
 #pragma unroll
-        for (uint32_t i = 0; i < kRouteTokens; ++i) {
+        for (int i = 0; i < kTok; ++i) {
+            double v = (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], d);
-            if (lane == 0 && i < nt) {
+            for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+            if (lane == 0 && (uint32_t)i < nt) {
                 uint32_t remote;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(logits + i * p.E + e)), "r"(0u));
-                asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(s[i]) : "memory");
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(&part[e][q])), "r"((uint32_t)i));
+                asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
             }
         }
     }
+    if (!waited) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    __syncwarp();
     cluster_sync();
-    if (rank != 0u) return;
-    // one warp per token: lane l holds experts l, l + 32, ...; k rounds of a warp argmax
-    for (uint32_t i = warp; i < nt; i += kRW) {
-        const double* lg = logits + i * p.E;
-        double top = -DBL_MAX, sum = 0.0;
-        bool bad = false;
-        for (uint32_t e = lane; e < p.E; e += 32u) {
-            bad |= !(fabs(lg[e]) <= DBL_MAX);
-            top = fmax(top, lg[e]);                                // a NaN is passed over
-        }
+    if (kDt == 0 && p.work.x16 != nullptr && rank >= kRouteTokens && rank - kRouteTokens < nt) {
+        __shared__ uint32_t red[64];
+        const uint32_t i = rank - kRouteTokens;
+        convert_row(x + (int64_t)i * p.ldx, p.H, p.work.x16 + (size_t)(t0 + i) * p.H, p.work.xd + t0 + i, red);
+    }
+    if (rank >= nt) return;
+    const size_t row = (size_t)(t0 + rank) * p.k;
+    uint32_t flags = 0u;
+    if (tid < p.E) {
+        const double v = (part[tid][0] + part[tid][1]) + (part[tid][2] + part[tid][3]);
+        if (!(fabs(v) <= DBL_MAX)) flags = kFlagNonFinite;
+        logit[tid] = v >= -DBL_MAX ? v : -DBL_MAX;                 // NaN and -inf rank last
+    }
+    __syncthreads();
+    // expert e by `per` threads, each comparing it with its share of the others
+    uint32_t lg = 0u;                                              // log2(per), per * E <= 512
+    while (lg < 4u && (p.E << (lg + 1u)) <= (uint32_t)kRouteThreads) ++lg;
+    const uint32_t e = tid >> lg, per = 1u << lg;
+    uint32_t above = 0u;
+    if (e < p.E) {
+        const double mine = logit[e];
+#pragma unroll 4
+        for (uint32_t o = tid & (per - 1u); o < p.E; o += per)
+            above += logit[o] > mine || (logit[o] == mine && o < e) ? 1u : 0u;
+    }
+    for (uint32_t d = 1u; d < per; d <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
+    if (e < p.E && above < p.k && (tid & (per - 1u)) == 0u) {
+        p.ids[row + above] = (int32_t)e;
+        chosen[above] = logit[e];
+    }
+    __syncthreads();
+    const double top = chosen[0];
+    if (p.renorm == 0u) {
+        double s = tid < p.E ? exp(logit[tid] - top) : 0.0;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        if (bad) flags |= kFlagNonFinite;
-        if (p.renorm == 0u) {
-            for (uint32_t e = lane; e < p.E; e += 32u) sum += exp(lg[e] - top);
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane == 0) sums[warp] = s;
+        __syncthreads();
+    }
+    if (warp == 0u) {
+        const double pj = lane < p.k ? exp(chosen[lane] - top) : 0.0;
+        double s = p.renorm != 0u ? pj : lane < kRW ? sums[lane] : 0.0;
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        }
-        uint64_t taken = 0ull;                                     // this lane's experts, one bit each (E <= 512)
-        int32_t my_id = 0;
-        double my_p = 0.0;
-        for (uint32_t j = 0; j < p.k; ++j) {
-            double v = -DBL_MAX;
-            uint32_t id = 0xFFFFFFFFu;
-            for (uint32_t e = lane, b = 0; e < p.E; e += 32u, ++b) {
-                if ((taken >> b) & 1ull) continue;
-                const double c = lg[e] >= -DBL_MAX ? lg[e] : -DBL_MAX;     // NaN and -inf rank last
-                if (id == 0xFFFFFFFFu || c > v) {
-                    v = c;
-                    id = e;
-                }
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                const double ov = __shfl_xor_sync(0xFFFFFFFFu, v, d);
-                const uint32_t oi = __shfl_xor_sync(0xFFFFFFFFu, id, d);
-                if (oi != 0xFFFFFFFFu && (id == 0xFFFFFFFFu || ov > v || (ov == v && oi < id))) {
-                    v = ov;
-                    id = oi;
-                }
-            }
-            if ((id & 31u) == lane) taken |= 1ull << (id >> 5);
-            const double pj = exp(lg[id] - top);
-            if (p.renorm != 0u) sum += pj;
-            if (lane == j) {                                       // k <= 32
-                my_id = (int32_t)id;
-                my_p = pj;
-            }
-        }
-        if (lane < p.k) {
-            p.ids[(size_t)(t0 + i) * p.k + lane] = my_id;
-            p.weights[(size_t)(t0 + i) * p.k + lane] = (float)(my_p / sum);
-        }
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane < p.k) p.weights[row + lane] = (float)(pj / s);
     }
     flags = __reduce_or_sync(0xFFFFFFFFu, flags);
     if (lane == 0) flag_or(p.d_flags, flags);
@@ -177,386 +270,495 @@ struct Experts {
     const float* weights;
     const uint8_t *gq, *gs, *uq, *us, *dq, *ds;   // codes and scales: gate, up [E, I, H], down [E, H, I]
     const float *g2, *u2, *d2;                    // [E]
-    float* h;                                     // workspace [T * k, I]
+    Work work;
     void* out;
     int64_t ldd;
     uint32_t T, k, E, H, I;
-    uint32_t smem_rows;                           // bytes of shared memory for token rows
 };
 
-// Which tokens chose which expert, built by every CTA for itself.  A pair is t * k + j; a token
-// that names an expert twice has it once, with both weights.
+// (What a kernel in front on the stream wrote is read with coherent loads: a CTA may have started
+// before it was written.)
+//
+// Which tokens chose which expert, built by every CTA for itself: a bit per token and expert, so
+// that a token that names an expert twice has it once, and the order is that of the tokens.
+// Rows: the (expert, token) pairs in that order; row r of h belongs to token tok[r].  Sub-lists:
+// up to 8 rows of one expert.
 struct Lists {
-    int32_t id[kMaxMoePairs];                     // the pair's expert, -1: none or named before
-    uint16_t pair[kMaxMoePairs];                  // pairs by expert, in token order
+    unsigned long long mask[kMaxMoeExperts];
+    uint8_t tok[kMaxMoePairs];
     uint16_t expert[kMaxMoeExperts];              // chosen experts in ascending order
-    uint16_t first[kMaxMoeExperts + 1];           // their first entry in pair[]
-    uint32_t scan[2][kWarps];
-    uint32_t n;                                   // chosen experts
+    uint16_t first[kMaxMoeExperts + 1];           // their first rows
+    uint16_t sub[kMaxMoeExperts + 1];             // and first sub-lists
+    uint16_t slot[kMaxMoeExperts];                // expert -> its place among the chosen
+    uint32_t scan[kWarps];
+    uint32_t n, subs;                             // chosen experts, sub-lists
+
+    // the chosen expert that sub-list s belongs to
+    __device__ __forceinline__ uint32_t find(uint32_t s) const
+    {
+        uint32_t a = 0u, b = n;                   // sub[a] <= s < sub[b]
+        while (b - a > 1u) {
+            const uint32_t m = (a + b) >> 1;
+            if (sub[m] <= s) a = m;
+            else b = m;
+        }
+        return a;
+    }
 };
 
 __device__ __forceinline__ void build_lists(Lists& L, const Experts& p)
 {
     const uint32_t P = p.T * p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    if (tid < p.E) L.mask[tid] = 0ull;
+    __syncthreads();
     for (uint32_t i = tid; i < P; i += kThreads) {
-        const int32_t e = __ldg(p.ids + i);
-        bool ok = e >= 0 && e < (int32_t)p.E;
-        for (uint32_t j = i - i % p.k; j < i; ++j) ok = ok && __ldg(p.ids + j) != e;
-        L.id[i] = ok ? e : -1;
+        const int32_t e = __ldcg(p.ids + i);
+        if (e >= 0 && e < (int32_t)p.E) atomicOr(&L.mask[e], 1ull << (i / p.k));
     }
     __syncthreads();
-    uint32_t cnt = 0u;
-    if (tid < p.E)
-        for (uint32_t i = 0; i < P; ++i) cnt += L.id[i] == (int32_t)tid ? 1u : 0u;
-    // exclusive scans over the experts: chosen ones and their pairs
-    uint32_t a = cnt != 0u ? 1u : 0u, b = cnt;
+    // exclusive scan over the experts of rows (at most 2048, bits 0-11), sub-lists (at most 768,
+    // bits 12-21) and chosen experts (at most 512, bits 22-31) in one word
+    unsigned long long mask = tid < p.E ? L.mask[tid] : 0ull;
+    const uint32_t cnt = (uint32_t)__popcll(mask), mine = cnt + (((cnt + 7u) >> 3) << 12) + (cnt != 0u ? 1u << 22 : 0u);
+    uint32_t a = mine;
 #pragma unroll
     for (uint32_t d = 1; d < 32; d <<= 1) {
-        const uint32_t oa = __shfl_up_sync(0xFFFFFFFFu, a, d), ob = __shfl_up_sync(0xFFFFFFFFu, b, d);
-        if (lane >= d) {
-            a += oa;
-            b += ob;
-        }
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, a, d);
+        if (lane >= d) a += o;
     }
-    if (lane == 31u) {
-        L.scan[0][warp] = a;
-        L.scan[1][warp] = b;
-    }
+    if (lane == 31u) L.scan[warp] = a;
     __syncthreads();
-    uint32_t ba = 0u, bb = 0u, n = 0u, np = 0u;
+    uint32_t total = 0u;
+#pragma unroll
     for (uint32_t w = 0; w < (uint32_t)kWarps; ++w) {
-        if (w < warp) {
-            ba += L.scan[0][w];
-            bb += L.scan[1][w];
-        }
-        n += L.scan[0][w];
-        np += L.scan[1][w];
+        const uint32_t v = L.scan[w];
+        if (w < warp) a += v;
+        total += v;
     }
+    a -= mine;
+    const uint32_t slot = a >> 22, at = a & 0xFFFu;
     if (cnt != 0u) {
-        const uint32_t slot = ba + a - 1u;
-        uint32_t at = bb + b - cnt;
         L.expert[slot] = (uint16_t)tid;
         L.first[slot] = (uint16_t)at;
-        for (uint32_t i = 0; i < P; ++i)
-            if (L.id[i] == (int32_t)tid) L.pair[at++] = (uint16_t)i;
+        L.sub[slot] = (uint16_t)((a >> 12) & 0x3FFu);
+        L.slot[tid] = (uint16_t)slot;
+        for (uint32_t i = 0; mask != 0ull; ++i, mask &= mask - 1ull) L.tok[at + i] = (uint8_t)(__ffsll((long long)mask) - 1);
     }
     if (tid == 0u) {
-        L.n = n;
-        L.first[n] = (uint16_t)np;
+        L.n = total >> 22;
+        L.subs = (total >> 12) & 0x3FFu;
+        L.first[total >> 22] = (uint16_t)(total & 0xFFFu);
+        L.sub[total >> 22] = (uint16_t)L.subs;
     }
     __syncthreads();
 }
 
 // ---------------------------------------------------------------- gate, up, SwiGLU
-// kNT: 8-token tiles of a pass (1 or 3).
-template <int kDt, bool kVec, int NT>
-__device__ __forceinline__ void up_pass(const Experts& p, const Lists& L, w4::Rows& rows, uint4* xs, float* red,
-                                        uint32_t e, uint32_t f0, uint32_t m, uint32_t i0, uint32_t i1)
-{
-    constexpr uint32_t kTile = 16u * 8u * NT;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
-    const uint32_t nch = (p.H + kChunk - 1u) / kChunk, R = i1 - i0, ntile = (R + 7u) / 8u;
-    const uint32_t wk = w4::split_of(ntile, nch), groups = kWarps / wk, grp = warp / wk, wig = warp - grp * wk;
-    const size_t mat = (size_t)e * p.I;
-    auto load = [&](Frag& f, uint32_t tile, uint32_t c) {
-        const uint32_t a = i0 + tile * R / ntile, b = i0 + (tile + 1u) * R / ntile, i = a + g;
-        const uint32_t k0 = c * kChunk + 64u * t;
-        const size_t q = (mat + i) * (p.H / 2u), s = (mat + i) * (p.H / 16u);
-        w4::load_row<kVec>(f.q0, f.s0, p.gq + q, p.gs + s, k0, p.H, i < b);
-        w4::load_row<kVec>(f.q1, f.s1, p.uq + q, p.us + s, k0, p.H, i < b);
-    };
-    Frag cur;
-    if (grp < ntile) load(cur, grp, wig);
-    __syncthreads();                                               // the previous pass has read its tokens
-    const bool wide = w4::stage_tokens<kDt>(xs, rows, m, p.H, [&](uint32_t i) {
-        return static_cast<const void*>(static_cast<const uint16_t*>(p.x) + (int64_t)(L.pair[f0 + i] / p.k) * p.ldx);
-    });
-    const float sg = p.g2[e], su = p.u2[e];
-    uint32_t buf = 0u;
-    for (uint32_t tile = grp; tile < ntile; tile += groups, buf ^= 1u) {
-        float acc[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-        for (uint32_t c = wig; c < nch; c += wk) {
-            Frag next;
-            const bool more = c + wk < nch;
-            if (more || tile + groups < ntile) load(next, more ? tile : tile + groups, more ? c + wk : wig);
-            const uint4* xc = xs + (size_t)c * 32u * m;
-            if (kDt == 0 && wide)
-                w4::mma_chunk<true, NT>(acc, cur, xc, m, g, t);
-            else
-                w4::mma_chunk<false, NT>(acc, cur, xc, m, g, t);
-            cur = next;
-        }
-        float* part = red + (size_t)(buf * kWarps + warp) * kTile;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            *reinterpret_cast<float2*>(part + g * (8 * NT) + 8 * j + 2 * t) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2*>(part + (g + 8) * (8 * NT) + 8 * j + 2 * t) = make_float2(acc[j][2], acc[j][3]);
-        }
-        if (wk == 1u) __syncwarp();
-        else w4::group_barrier(1u + grp, 32u * wk);
-        const uint32_t a = i0 + tile * R / ntile, nr = i0 + (tile + 1u) * R / ntile - a;
-        const float* first = red + (size_t)(buf * kWarps + grp * wk) * kTile;
-        for (uint32_t i = wig * 32u + lane; i < 8u * m; i += 32u * wk) {
-            const uint32_t r = i & 7u, tok = i >> 3;
-            if (r >= nr) continue;
-            float sa = 0.0f, sb = 0.0f;
-            for (uint32_t w = 0; w < wk; ++w) {
-                sa += first[(size_t)w * kTile + r * (8 * NT) + tok];
-                sb += first[(size_t)w * kTile + (r + 8u) * (8 * NT) + tok];
-            }
-            const float gv = sa * sg * rows.descale[tok], uv = sb * su * rows.descale[tok];
-            p.h[(size_t)L.pair[f0 + tok] * p.I + a + r] = gv / (1.0f + expf(-gv)) * uv;
-        }
-    }
-}
+constexpr uint32_t kMaxSegs = 8;
+
+// A run of row pairs of one sub-list in a CTA's range, in tiles of th pairs from tile0 on; its
+// tokens are rows f0 .. f0 + m - 1 of the lists.
+struct Seg {
+    uint32_t expert, f0, m, i0, n, th, tile0;
+    float sg, su;
+};
+
+struct Segs {
+    Seg s[kMaxSegs];
+    uint32_t n, ntile, pairs;
+};
 
 template <int kDt, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ Experts p)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];                // the warps' rings
     __shared__ Lists L;
-    __shared__ w4::Rows rows;
-    uint4* xs = reinterpret_cast<uint4*>(smem);
-    float* red = reinterpret_cast<float*>(smem + p.smem_rows);
+    __shared__ Segs S;
+    __shared__ __align__(16) float red[2][kWarps][16 * 8];
+    __shared__ float descale[kMaxMoeTokens];
+    constexpr uint32_t kTile = 16u * 8u;
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
+    const uint32_t nch = (p.H + kChunk - 1u) / kChunk;
+    w4::pdl_wait();                                                // ids are the router's
+    w4::pdl_launch();
+    // BF16 rows: their FP16 form, unless some row has none: then all as they are
+    float d = 1.0f;
+    if (kDt == 0 && tid < p.T) d = p.work.xd[tid];
+    const bool wide = __syncthreads_or(d < 0.0f) != 0;
+    if (tid < p.T) descale[tid] = wide ? 1.0f : d;
+    const uint16_t* x = kDt == 1 || wide ? static_cast<const uint16_t*>(p.x) : p.work.x16;
+    const int64_t ldx = kDt == 1 || wide ? p.ldx : (int64_t)p.H;
     build_lists(L, p);
-    const uint64_t total = (uint64_t)L.n * p.I;
-    const uint64_t end = (blockIdx.x + 1u) * total / gridDim.x;
-    const uint32_t cap = min(kPass, p.smem_rows / ((p.H + kChunk - 1u) / kChunk * 512u));
-    for (uint64_t at = blockIdx.x * total / gridDim.x; at < end;) {
-        const uint32_t a = (uint32_t)(at / p.I), i0 = (uint32_t)(at - (uint64_t)a * p.I);
-        const uint32_t i1 = (uint32_t)min((uint64_t)p.I, end - (uint64_t)a * p.I);
-        const uint32_t f0 = L.first[a], m_e = L.first[a + 1u] - f0;
-        for (uint32_t q = 0; q < m_e; q += cap) {
-            const uint32_t m = min(cap, m_e - q);
-            if (m <= 8u) up_pass<kDt, kVec, 1>(p, L, rows, xs, red, L.expert[a], f0 + q, m, i0, i1);
-            else up_pass<kDt, kVec, 3>(p, L, rows, xs, red, L.expert[a], f0 + q, m, i0, i1);
+    const uint32_t total = L.subs * p.I;                           // at most 768 x 2^15
+    uint32_t at = (uint32_t)((uint64_t)blockIdx.x * total / gridDim.x);
+    const uint32_t end = (uint32_t)((uint64_t)(blockIdx.x + 1u) * total / gridDim.x);
+    while (at < end) {
+        if (tid == 0u) {
+            uint32_t n = 0u, nt = 0u, w = at, s = w / p.I, a = L.find(s);
+            while (w < end && n < kMaxSegs) {
+                Seg& sg = S.s[n];
+                sg.expert = L.expert[a];
+                sg.f0 = L.first[a] + (s - L.sub[a]) * kPass;
+                sg.m = min(kPass, L.first[a + 1u] - sg.f0);
+                sg.i0 = w - s * p.I;
+                sg.n = min(p.I - sg.i0, end - w);
+                const uint32_t tiles = (sg.n + 7u) / 8u;
+                sg.th = (sg.n + tiles - 1u) / tiles;
+                sg.tile0 = nt;
+                sg.sg = __ldg(p.g2 + sg.expert);
+                sg.su = __ldg(p.u2 + sg.expert);
+                nt += (sg.n + sg.th - 1u) / sg.th;
+                w += sg.n;
+                ++n;
+                ++s;
+                if (s >= L.sub[a + 1u]) ++a;
+            }
+            S.n = n;
+            S.ntile = nt;
+            S.pairs = w - at;
         }
-        at = (uint64_t)a * p.I + i1;
+        __syncthreads();
+        const uint32_t wk = w4::split_of(S.ntile, nch), groups = kWarps / wk, grp = warp / wk, wig = warp - grp * wk;
+        const uint32_t my_tiles = grp < S.ntile ? (S.ntile - grp + groups - 1u) / groups : 0u;
+        const uint32_t steps = my_tiles * (wig < nch ? (nch - wig + wk - 1u) / wk : 0u);
+        uint32_t lt = grp, lc = wig, ls = 0u;
+        size_t row = 0;                                            // byte offset of this lane's row pair
+        bool live = false, moved = true;
+        auto load = [&](uint8_t* slot) {
+            if (moved) {
+                while (ls + 1u < S.n && lt >= S.s[ls + 1u].tile0) ++ls;
+                const Seg& sg = S.s[ls];
+                const uint32_t i = (lt - sg.tile0) * sg.th + g;
+                live = g < sg.th && i < sg.n;
+                row = ((size_t)sg.expert * p.I + sg.i0 + i) * (p.H / 2u);
+                moved = false;
+            }
+            w4::load_chunk<kVec>(slot, p.gq + row, p.gs + row / 8u, p.uq + row, p.us + row / 8u, lc, p.H, live, live);
+            lc += wk;
+            if (lc >= nch) {
+                lc = wig;
+                lt += groups;
+                moved = true;
+            }
+        };
+        w4::Ring ring;
+        ring.begin(smem + warp * (w4::kDepth * w4::kSlot), steps, load);
+        w4::Acc<1> acc;
+        w4::clear<1>(acc);
+        uint32_t ut = grp, uc = wig, us = 0u, buf = 0u;
+        const uint16_t* xr = nullptr;                              // column g's token row
+        ring.run(load, [&](const uint8_t* slot) {
+            if (uc == wig) {
+                while (us + 1u < S.n && ut >= S.s[us + 1u].tile0) ++us;
+                xr = x + (int64_t)L.tok[S.s[us].f0 + min(g, S.s[us].m - 1u)] * ldx;
+            }
+            if (kDt == 0 && wide) w4::mma_chunk_global<true>(acc, slot, xr, uc * kChunk, p.H);
+            else w4::mma_chunk_global<false>(acc, slot, xr, uc * kChunk, p.H);
+            uc += wk;
+            if (uc < nch) return;
+            w4::put_part<1>(red[buf][warp], acc, g, t);
+            w4::clear<1>(acc);
+            w4::group_barrier(grp, wk);
+            const Seg& sg = S.s[us];
+            const uint32_t a = (ut - sg.tile0) * sg.th, nr = min(sg.th, sg.n - a);
+            const float* first = red[buf][grp * wk];
+            for (uint32_t i = wig * 32u + lane; i < 8u * sg.m; i += 32u * wk) {
+                const uint32_t r = i & 7u, col = i >> 3, hr = sg.f0 + col;
+                if (r >= nr) continue;
+                const float ds = descale[L.tok[hr]];
+                const float gv = w4::sum_parts<kTile>(first + r * 8u + col, wk) * sg.sg * ds;
+                const float uv = w4::sum_parts<kTile>(first + (r + 8u) * 8u + col, wk) * sg.su * ds;
+                p.work.h[(size_t)hr * p.I + sg.i0 + a + r] = gv / (1.0f + expf(-gv)) * uv;
+            }
+            buf ^= 1u;
+            uc = wig;
+            ut += groups;
+        });
+        at += S.pairs;
+        __syncthreads();                                           // S and the sums are free
     }
+}
+
+// ---------------------------------------------------------------- h to FP16
+// One CTA per row (rows that no pair has are converted too, and read by nothing).
+__global__ void __launch_bounds__(256) moe_hidden_kernel(const __grid_constant__ Experts p)
+{
+    __shared__ uint32_t red[8];
+    w4::pdl_wait();
+    w4::pdl_launch();
+    const uint32_t tid = threadIdx.x;
+    const float4* src = reinterpret_cast<const float4*>(p.work.h + (size_t)blockIdx.x * p.I);
+    constexpr int kKeep = 2;                                       // 8 values each
+    float4 keep[kKeep][2];
+    uint32_t top = 0u;
+    auto scan = [&](const float4& v) {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+            if (b < 0x7F800000u) top = max(top, b);                // the largest finite magnitude
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const uint32_t v = tid + 256u * i;
+        keep[i][0] = keep[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (8u * v < p.I) {
+            keep[i][0] = src[2u * v];
+            keep[i][1] = src[2u * v + 1u];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        scan(keep[i][0]);
+        scan(keep[i][1]);
+    }
+    for (uint32_t v = tid + 256u * kKeep; 8u * v < p.I; v += 256u) {
+        scan(src[2u * v]);
+        scan(src[2u * v + 1u]);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((tid & 31u) == 0u) red[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = max(top, red[w]);
+    const int e1 = (int)(top >> 23), fe = top == 0u ? 127 : min(268 - e1, 254);     // factor 2^(fe - 127): largest to 2^14
+    const float f = w4::exp_field(fe);
+    if (tid == 0u) p.work.hd[blockIdx.x] = w4::exp_field(254 - fe);
+    auto put = [&](uint32_t v, const float4& a, const float4& b) {
+        const float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(__fmul_rn(z[2 * j + 1], f)), "f"(__fmul_rn(z[2 * j], f)));
+        *reinterpret_cast<uint4*>(p.work.h16 + (size_t)blockIdx.x * p.I + 8u * v) = make_uint4(o[0], o[1], o[2], o[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (8u * (tid + 256u * i) < p.I) put(tid + 256u * i, keep[i][0], keep[i][1]);
+    for (uint32_t v = tid + 256u * kKeep; 8u * v < p.I; v += 256u) put(v, src[2u * v], src[2u * v + 1u]);
 }
 
 // ---------------------------------------------------------------- down, weighted sum
-constexpr uint32_t kMaxSubs = 32;                 // (expert, up to kPass of its tokens) staged at once
-
-struct Batch {
-    uint16_t expert[kMaxSubs], first[kMaxSubs], m[kMaxSubs], row0[kMaxSubs];
-    uint32_t n, rows, next_a, next_q;
-};
-
-// One sub-list's product: acc over chunks [c0, c1) of a 16-row tile, added into this warp's
-// sums Y[token][16], each token's column times its coefficient.
-template <bool kVec, int NT>
-__device__ __forceinline__ void down_run(const Experts& p, const Lists& L, const float* coef, float* Y,
-                                         const uint4* xs, uint32_t m, uint32_t f0, const uint8_t* q, const uint8_t* s,
-                                         bool la, bool lb, uint32_t c0, uint32_t c1)
-{
-    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    Frag cur, next;
-    const size_t q8 = (size_t)8u * (p.I / 2u), s8 = (size_t)8u * (p.I / 16u);
-    auto load = [&](Frag& f, uint32_t c) {
-        const uint32_t k0 = c * kChunk + 64u * t;
-        w4::load_row<kVec>(f.q0, f.s0, q, s, k0, p.I, la);
-        w4::load_row<kVec>(f.q1, f.s1, q + q8, s + s8, k0, p.I, lb);
-    };
-    load(cur, c0);
-    for (uint32_t c = c0; c < c1; ++c) {
-        if (c + 1u < c1) load(next, c + 1u);
-        w4::mma_chunk<false, NT>(acc, cur, xs + (size_t)c * 32u * m, m, g, t);
-        cur = next;
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-            const uint32_t col = 8u * j + 2u * t + i;
-            if (col < m) {
-                float* y = Y + (size_t)(L.pair[f0 + col] / p.k) * 16u;
-                y[g] += acc[j][i] * coef[col];
-                y[g + 8] += acc[j][2 + i] * coef[col];
-            }
-        }
-    __syncwarp();
-}
-
 template <int kOut, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ Experts p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Lists L;
-    __shared__ Batch B;
-    __shared__ float coef[kMaxSubs * kPass];
-    uint4* xs = reinterpret_cast<uint4*>(smem);
-    float* Yall = reinterpret_cast<float*>(smem + p.smem_rows);    // [16 warps][T][16]
-    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2;
-    build_lists(L, p);
+    __shared__ float coef[kMaxMoePairs];                           // routing weight x expert scale x row scale
+    float* Yall = reinterpret_cast<float*>(smem + w4::kRing);      // [16 warps][T][16]
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const uint32_t r0 = (uint32_t)((uint64_t)blockIdx.x * p.H / gridDim.x);
     const uint32_t R = (uint32_t)((uint64_t)(blockIdx.x + 1u) * p.H / gridDim.x) - r0;
-    const uint32_t ntile = (R + 15u) / 16u;                        // at most 16: H <= 256 x CTAs
+    const uint32_t ntile = (R + 15u) / 16u, th = (R + ntile - 1u) / ntile;      // at most 16 tiles: H <= 256 x CTAs
     const uint32_t wpt = kWarps / ntile, tile = warp % ntile, widx = warp / ntile;
+    const uint32_t ta = tile * th, tn = ta < R ? min(th, R - ta) : 0u;
     const bool works = widx < wpt;
-    const uint32_t ta = r0 + tile * R / ntile, tb = r0 + (tile + 1u) * R / ntile;
     float* Y = Yall + (size_t)warp * p.T * 16u;
     for (uint32_t i = lane; i < p.T * 16u; i += 32u) Y[i] = 0.0f;
-    const uint32_t nch = (p.I + kChunk - 1u) / kChunk, row_vecs = nch * 32u;
-    const uint32_t cap_rows = min(kMaxSubs * kPass, p.smem_rows / (row_vecs * 16u)), cap = min(kPass, cap_rows);
-    if (tid == 0u) B.next_a = B.next_q = 0u;
-
-    for (;;) {
-        __syncthreads();                                           // the previous batch has been used
-        if (tid == 0u) {                                           // the next batch: whole sub-lists while they fit
-            uint32_t n = 0u, rows = 0u, a = B.next_a, q = B.next_q;
-            while (a < L.n && n < kMaxSubs) {
-                const uint32_t m = min(cap, (uint32_t)L.first[a + 1u] - L.first[a] - q);
-                if (rows + m > cap_rows) break;
-                B.expert[n] = L.expert[a];
-                B.first[n] = (uint16_t)(L.first[a] + q);
-                B.m[n] = (uint16_t)m;
-                B.row0[n] = (uint16_t)rows;
-                rows += m;
-                ++n;
-                q += m;
-                if (q == (uint32_t)L.first[a + 1u] - L.first[a]) {
-                    ++a;
-                    q = 0u;
-                }
-            }
-            B.n = n;
-            B.rows = rows;
-            B.next_a = a;
-            B.next_q = q;
+    const uint32_t nch = (p.I + kChunk - 1u) / kChunk;
+    // ids and weights were written before the two kernels in front of this one began
+    build_lists(L, p);
+    for (uint32_t i = tid; i < p.T * p.k; i += kThreads) {
+        const uint32_t tok = i / p.k, j0 = tok * p.k;
+        const int32_t e = __ldcg(p.ids + i);
+        if (e < 0 || e >= (int32_t)p.E) continue;
+        float w = 0.0f;
+        bool first = true;                                         // the token's first mention of the expert: all its weights
+        for (uint32_t j = j0; j < j0 + p.k; ++j) {
+            const bool same = __ldcg(p.ids + j) == e;
+            if (same && j < i) first = false;
+            if (same) w += __ldcg(p.weights + j);
         }
-        __syncthreads();
-        const uint32_t n = B.n;
-        if (n == 0u) break;
-        // ---- h rows: one warp per row; scaled by a power of two to FP16
-        for (uint32_t r = warp; r < B.rows; r += kWarps) {
-            uint32_t s = 0u;
-            while (s + 1u < n && r >= B.row0[s + 1u]) ++s;
-            const uint32_t i = r - B.row0[s], m = B.m[s], pr = L.pair[B.first[s] + i];
-            const float4* src = reinterpret_cast<const float4*>(p.h + (size_t)pr * p.I);
-            uint32_t top = 0u;
-            for (uint32_t k = 4u * lane; k < p.I; k += 128u) {
-                const float4 v = src[k >> 2];
-                const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
-                    if (b < 0x7F800000u) top = max(top, b);        // the largest finite one
-                }
-            }
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            const int e1 = (int)(top >> 23);
-            const int fe = top == 0u ? 127 : min(268 - e1, 254);   // factor 2^(fe - 127)
-            const float f = w4::exp_field(fe);
-            uint4* dst = xs + (size_t)B.row0[s] * row_vecs;
-            for (uint32_t v8 = lane; v8 < row_vecs; v8 += 32u) {
-                const uint32_t c = v8 >> 5, l = v8 & 31u, k = c * kChunk + 8u * l;
-                uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                if (k < p.I) {
-                    const float4 u = src[k >> 2], v = src[(k >> 2) + 1u];
-                    const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-                    uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                            : "=r"(ow[j])
-                            : "f"(__fmul_rn(w[2 * j + 1], f)), "f"(__fmul_rn(w[2 * j], f)));
-                }
-                dst[((c * 8u + (l & 7u)) * m + i) * 4u + (l >> 3)] = o;
-            }
-            if (lane == 0u) {
-                const uint32_t tok = pr / p.k;
-                const int32_t e = L.id[pr];
-                float w = 0.0f;                                    // a token's weights of this expert
-                for (uint32_t j = 0; j < p.k; ++j)
-                    if (__ldg(p.ids + tok * p.k + j) == e) w += __ldg(p.weights + tok * p.k + j);
-                coef[r] = w * p.d2[e] * w4::exp_field(254 - fe);
-            }
-        }
-        __syncthreads();
-        // ---- products: (sub-list, chunk) steps in a contiguous run per warp
-        if (works) {
-            const uint32_t steps = n * nch, b = (widx + 1u) * steps / wpt;
-            for (uint32_t at = widx * steps / wpt; at < b;) {
-                const uint32_t s = at / nch, c0 = at - s * nch, c1 = min(nch, b - s * nch), m = B.m[s];
-                const size_t row = (size_t)B.expert[s] * p.H + ta + g;
-                const uint8_t* q = p.dq + row * (p.I / 2u);
-                const uint8_t* sc = p.ds + row * (p.I / 16u);
-                const uint4* xb = xs + (size_t)B.row0[s] * row_vecs;
-                const bool la = ta + g < tb, lb = ta + g + 8u < tb;
-                if (m <= 8u) down_run<kVec, 1>(p, L, coef + B.row0[s], Y, xb, m, B.first[s], q, sc, la, lb, c0, c1);
-                else down_run<kVec, 3>(p, L, coef + B.row0[s], Y, xb, m, B.first[s], q, sc, la, lb, c0, c1);
-                at = s * nch + c1;
-            }
-        }
+        if (first) coef[L.first[L.slot[e]] + __popcll(L.mask[e] & ((1ull << tok) - 1ull))] = w * __ldg(p.d2 + e);
     }
-    // ---- the warps' sums of a tile, in warp order (the loop ended behind a CTA barrier)
+    // this warp's run of the tile's (sub-list, chunk) steps
+    const uint32_t n = L.subs * nch, s0 = works ? (uint32_t)((uint64_t)widx * n / wpt) : 0u;
+    const uint32_t steps = works ? (uint32_t)((uint64_t)(widx + 1u) * n / wpt) - s0 : 0u;
+    uint32_t us = s0 / nch, uc = s0 - us * nch, ua = steps != 0u ? L.find(us) : 0u;
+    uint32_t ls = us, lc = uc, la = ua;
+    size_t row = 0;
+    bool moved = true;
+    auto load = [&](uint8_t* slot) {
+        if (moved) {
+            if (ls >= L.sub[la + 1u]) ++la;
+            row = ((size_t)L.expert[la] * p.H + r0 + ta + g) * (p.I / 2u);
+            moved = false;
+        }
+        const size_t row8 = row + (size_t)8u * (p.I / 2u);
+        w4::load_chunk<kVec>(slot, p.dq + row, p.ds + row / 8u, p.dq + row8, p.ds + row8 / 8u, lc, p.I, g < tn, g + 8u < tn);
+        if (++lc == nch) {
+            lc = 0u;
+            ++ls;
+            moved = true;
+        }
+    };
+    w4::Ring ring;
+    ring.begin(smem + warp * (w4::kDepth * w4::kSlot), steps, load);
+    w4::pdl_wait();                                                // h is complete
+    __syncthreads();                                               // coef
+    for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) coef[i] *= p.work.hd[i];
+    __syncthreads();
+    w4::Acc<1> acc;
+    w4::clear<1>(acc);
+    uint32_t left = steps, f0 = 0u, m = 0u;
+    const uint16_t* xr = nullptr;
+    bool fresh = true;
+    ring.run(load, [&](const uint8_t* slot) {
+        if (fresh) {
+            if (us >= L.sub[ua + 1u]) ++ua;
+            f0 = L.first[ua] + (us - L.sub[ua]) * kPass;
+            m = min(kPass, L.first[ua + 1u] - f0);
+            xr = p.work.h16 + (size_t)(f0 + min(g, m - 1u)) * p.I;
+            fresh = false;
+        }
+        w4::mma_chunk_global<false>(acc, slot, xr, uc * kChunk, p.I);
+        --left;
+        if (++uc < nch && left != 0u) return;
+        // the sub-list's end: its columns, each times its coefficient, into the warp's sums
+        w4::join<1>(acc);
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+            const uint32_t col = 2u * t + i;
+            if (col < m) {
+                float* y = Y + (size_t)L.tok[f0 + col] * 16u;
+                y[g] += acc[0][0][i] * coef[f0 + col];
+                y[g + 8] += acc[0][0][2 + i] * coef[f0 + col];
+            }
+        }
+        __syncwarp();
+        w4::clear<1>(acc);
+        uc = 0u;
+        ++us;
+        fresh = true;
+    });
+    __syncthreads();
+    // ---- the warps' sums of a tile, in warp order
     for (uint32_t i = tid; i < p.T * R; i += kThreads) {
-        const uint32_t tok = i / R, r = i - tok * R;
-        uint32_t tl = r * ntile / R;                               // the tile that holds row r
-        while (r < tl * R / ntile) --tl;
-        while (r >= (tl + 1u) * R / ntile) ++tl;
-        const uint32_t in = r - tl * R / ntile;
+        const uint32_t tok = i / R, r = i - tok * R, tl = r / th, in = r - tl * th;
         float v = 0.0f;
+#pragma unroll 4
         for (uint32_t w = 0; w < wpt; ++w) v += Yall[((size_t)(w * ntile + tl) * p.T + tok) * 16u + in];
         w4::store_out<kOut>(p.out, (int64_t)tok * p.ldd + r0 + r, v);
     }
 }
 
-}  // namespace moe
-
-cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_t ldx, const void* wr, int64_t E,
-                             int top_k, int renorm, int32_t* ids, float* weights, uint32_t* d_flags, cudaStream_t s)
+template <class Kern, class P>
+static cudaError_t launch(Kern kern, const P& p, uint32_t grid, uint32_t threads, size_t smem, uint32_t cluster, bool dependent,
+                          cudaStream_t s)
 {
-    using namespace moe;
-    RouteParams p{x, ldx, wr, ids, weights, (uint32_t)T, (uint32_t)H, (uint32_t)E, (uint32_t)top_k, (uint32_t)renorm, d_flags};
-    const unsigned grid = (unsigned)((T + kRouteTokens - 1) / kRouteTokens) * kRouteCtas;
-    const size_t smem = (size_t)kRouteTokens * E * sizeof(double);
-    if (dt == 0) moe_route_kernel<0><<<grid, kRouteThreads, smem, s>>>(p);
-    else moe_route_kernel<1><<<grid, kRouteThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1u) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (dependent) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_moe_experts(const MoeExpertsArgs& a, cudaStream_t s)
+// Once per kernel and device: its shared memory limit, and clusters of 16.
+template <class Kern>
+static cudaError_t prepare(Kern kern, bool (&ready)[64], int smem, bool cluster16)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && ready[dev]) return cudaSuccess;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && cluster16) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev] = true;
+    return e;
+}
+
+template <int kDt, int kTok>
+static cudaError_t run_route(const RouteParams& p, cudaStream_t s)
+{
+    static bool ready[64] = {};
+    const cudaError_t e = prepare(moe_route_kernel<kDt, kTok>, ready, 0, true);
+    if (e != cudaSuccess) return e;
+    return launch(moe_route_kernel<kDt, kTok>, p, (p.T + kTok - 1u) / kTok * kRouteCtas, kRouteThreads, 0, kRouteCtas, false, s);
+}
+
+template <int kDt, bool kVec>
+static cudaError_t run_up(const Experts& p, bool dependent, cudaStream_t s)
+{
+    static bool ready[64] = {};
+    const cudaError_t e = prepare(moe_up_kernel<kDt, kVec>, ready, (int)w4::kRing, false);
+    if (e != cudaSuccess) return e;
+    return launch(moe_up_kernel<kDt, kVec>, p, (uint32_t)num_sms(), kThreads, w4::kRing, 1u, dependent, s);
+}
+
+template <int kOut, bool kVec>
+static cudaError_t run_down(const Experts& p, cudaStream_t s)
+{
+    static bool ready[64] = {};
+    const uint32_t sms = (uint32_t)num_sms(), grid = p.H < sms ? p.H : sms;
+    if ((p.H + grid - 1u) / grid > 16u * kWarps) return cudaErrorInvalidValue;
+    constexpr uint32_t most = kWarps * (uint32_t)kMaxMoeTokens * 16u * (uint32_t)sizeof(float);
+    const cudaError_t e = prepare(moe_down_kernel<kOut, kVec>, ready, (int)(w4::kRing + most), false);
+    if (e != cudaSuccess) return e;
+    return launch(moe_down_kernel<kOut, kVec>, p, grid, kThreads, w4::kRing + kWarps * (size_t)p.T * 16u * sizeof(float), 1u, true,
+                  s);
+}
+
+}  // namespace moe
+
+size_t moe_work_bytes(int64_t T, int64_t k, int64_t H, int64_t I)
+{
+    size_t n = 0;
+    (void)moe::work_of(nullptr, (size_t)T, (size_t)k, (size_t)H, (size_t)I, &n);
+    return n;
+}
+
+cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_t ldx, const void* wr, int64_t E,
+                             int top_k, int renorm, int32_t* ids, float* weights, const MoeExpertsArgs* then,
+                             uint32_t* d_flags, cudaStream_t s)
 {
     using namespace moe;
-    Experts p{a.x, a.ldx, a.ids, a.weights, a.gq, a.gs, a.uq, a.us, a.dq, a.ds, a.g2, a.u2, a.d2, a.h, a.out, a.ldd,
-              (uint32_t)a.T, (uint32_t)a.k, (uint32_t)a.E, (uint32_t)a.H, (uint32_t)a.I, 0u};
-    auto vec = [](const void* q, const void* sc) {
-        return (reinterpret_cast<uintptr_t>(q) & 31u) == 0u && (reinterpret_cast<uintptr_t>(sc) & 3u) == 0u;
-    };
-    const uint32_t sms = (uint32_t)num_sms();
-    {
-        const uint32_t red = 2u * kWarps * 16u * kPass * (uint32_t)sizeof(float);
-        p.smem_rows = (uint32_t)(kMaxSmemMoe - red) & ~511u;
-        const bool v = a.H % 64 == 0 && vec(a.gq, a.gs) && vec(a.uq, a.us);
-        auto kern = a.dt == 0 ? (v ? moe_up_kernel<0, true> : moe_up_kernel<0, false>)
-                              : (v ? moe_up_kernel<1, true> : moe_up_kernel<1, false>);
-        const size_t smem = (size_t)p.smem_rows + red;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        kern<<<sms, kThreads, smem, s>>>(p);
-        e = cudaGetLastError();
+    RouteParams p{x, ldx, wr, ids, weights, (uint32_t)T, (uint32_t)H, (uint32_t)E, (uint32_t)top_k, (uint32_t)renorm, d_flags, {}};
+    size_t n;
+    if (then != nullptr) p.work = work_of(then->work, (size_t)T, (size_t)top_k, (size_t)H, (size_t)then->I, &n);
+    if (T == 1) return dt == 0 ? run_route<0, 1>(p, s) : run_route<1, 1>(p, s);
+    return dt == 0 ? run_route<0, kRouteTokens>(p, s) : run_route<1, kRouteTokens>(p, s);
+}
+
+cudaError_t launch_moe_experts(const MoeExpertsArgs& a, bool routed, cudaStream_t s)
+{
+    using namespace moe;
+    size_t n;
+    const Experts p{a.x, a.ldx, a.ids, a.weights, a.gq, a.gs, a.uq, a.us, a.dq, a.ds, a.g2, a.u2, a.d2,
+                    work_of(a.work, (size_t)a.T, (size_t)a.k, (size_t)a.H, (size_t)a.I, &n), a.out, a.ldd,
+                    (uint32_t)a.T, (uint32_t)a.k, (uint32_t)a.E, (uint32_t)a.H, (uint32_t)a.I};
+    if (!routed && a.dt == 0) {
+        moe_rows_kernel<<<(unsigned)a.T, 512, 0, s>>>(a.x, a.ldx, p.H, p.work);
+        const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const uint32_t grid = (uint32_t)a.H < sms ? (uint32_t)a.H : sms;
-    if (((uint32_t)a.H + grid - 1u) / grid > 16u * kWarps) return cudaErrorInvalidValue;
-    const uint32_t sums = kWarps * (uint32_t)a.T * 16u * (uint32_t)sizeof(float);
-    p.smem_rows = (uint32_t)(kMaxSmemMoe - sums) & ~511u;
-    const bool v = a.I % 64 == 0 && vec(a.dq, a.ds);
-    auto kern = a.out_dt == 0 ? (v ? moe_down_kernel<0, true> : moe_down_kernel<0, false>)
-                              : a.out_dt == 1 ? (v ? moe_down_kernel<1, true> : moe_down_kernel<1, false>)
-                                              : (v ? moe_down_kernel<2, true> : moe_down_kernel<2, false>);
-    const size_t smem = (size_t)p.smem_rows + sums;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const bool dep = routed || a.dt == 0;                          // behind the router or moe_rows_kernel
+    const bool vu = a.H % 64 == 0, vd = a.I % 64 == 0;             // (the scales are 16-byte aligned)
+    cudaError_t e = a.dt == 0 ? (vu ? run_up<0, true>(p, dep, s) : run_up<0, false>(p, dep, s))
+                              : (vu ? run_up<1, true>(p, dep, s) : run_up<1, false>(p, dep, s));
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    e = launch(moe_hidden_kernel, p, p.T * p.k, 256u, 0, 1u, true, s);
+    if (e != cudaSuccess) return e;
+    if (a.out_dt == 0) return vd ? run_down<0, true>(p, s) : run_down<0, false>(p, s);
+    if (a.out_dt == 1) return vd ? run_down<1, true>(p, s) : run_down<1, false>(p, s);
+    return vd ? run_down<2, true>(p, s) : run_down<2, false>(p, s);
 }
 
 }  // namespace nv4

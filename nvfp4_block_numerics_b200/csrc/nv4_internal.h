@@ -93,10 +93,9 @@ cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
                                 cudaStream_t s);
 // Mixture-of-experts limits: tokens and (token, expert) pairs of a call, experts, experts per
-// token, widths (a token row of K <= 32768 beside the partial sums in shared memory).
+// token, widths.
 constexpr int64_t kMaxMoeTokens = 64, kMaxMoePairs = 2048, kMaxMoeExperts = 512, kMaxMoeTopK = 32;
 constexpr int64_t kMaxMoeWidth = 32768;
-constexpr size_t kMaxSmemMoe = 208u * 1024u;
 struct MoeExpertsArgs {
     const void* x;
     int dt, out_dt;
@@ -105,12 +104,15 @@ struct MoeExpertsArgs {
     const float* weights;
     const uint8_t *gq, *gs, *uq, *us, *dq, *ds;
     const float *g2, *u2, *d2;
-    float* h;
+    void* work;
     void* out;
 };
+size_t moe_work_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
 cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_t ldx, const void* wr, int64_t E,
-                             int top_k, int renorm, int32_t* ids, float* weights, uint32_t* d_flags, cudaStream_t s);
-cudaError_t launch_moe_experts(const MoeExpertsArgs& a, cudaStream_t s);
+                             int top_k, int renorm, int32_t* ids, float* weights, const MoeExpertsArgs* then,
+                             uint32_t* d_flags, cudaStream_t s);
+// routed: the call in front on the stream is launch_moe_route with these arguments as `then`.
+cudaError_t launch_moe_experts(const MoeExpertsArgs& a, bool routed, cudaStream_t s);
 cudaError_t launch_mxfp4_quant_mma(const void* x, int in_dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
                                    uint8_t* sf, uint32_t* d_flags, cudaStream_t s);
 cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,

@@ -3,23 +3,31 @@
 //
 // A warp multiplies 16 weight rows by up to 8 * NT token rows over K in chunks of 256, with
 // mma.m16n8k16 (weights are the 16-row operand, tokens the 8-column one).  Lane (g, t) of the
-// warp (g = lane / 4, t = lane % 4) holds 64 consecutive K-elements of weight rows g and g + 8,
-// loaded straight from global memory (32 bytes of codes, 4 block scales each), and feeds them to
-// 16 MMA steps of 4 elements: a dot product does not care which K-element sits in which MMA
-// slot as long as both operands agree, so the codes need no shuffling and no shared memory.
+// warp (g = lane / 4, t = lane % 4) holds 64 elements of a chunk of weight rows g and g + 8, 32
+// consecutive ones of either half, and feeds them to 16 MMA steps of 4 elements: a dot product
+// does not care which K-element sits in which MMA slot as long as both operands agree, so the
+// codes need no shuffling.
+//
+// The weights stream through a ring in shared memory that each warp fills for itself with
+// cp.async, kDepth chunks ahead, across the ends of tiles: no barrier, no register holds what is
+// in flight, and the loop stays small (with the ring in registers, three chunks unrolled, every
+// launch paid for fetching the code: 16 warps took 2600 clocks for their first chunks).
+//
 // e2m1 * e4m3 has at most 6 significant bits and lies on multiples of 2^-10 below 2688: exact
 // in FP16, so a weight is decoded by one conversion (cvt.rn.f16x2.e2m1x2, two codes) and one
 // multiply; measured in registers alone 15.8 T weights/s against the 11.6 T/s that HBM can
 // deliver.  The same through BF16 (mask and shift, bf16x2 multiply) gives 9.4 T/s, below it.
-// So the token rows are FP16 too.  FP16 rows are taken as they are.  BF16 rows are scaled by a
-// power of two per row (largest exponent to 2^14) and converted: exact for elements down to
-// 2^-31 of the row's largest (8 significant bits above the last FP16 bit, 2^-24).  A row that
-// spans more, or holds a NaN, an Inf or a BF16 subnormal, switches its whole pass to BF16
-// operands (kWide: the same codes, converted once more), which is exact for every input.
+// So the token rows are FP16 too.  FP16 rows are taken as they are.  BF16 rows are multiplied by
+// 2^4 and converted, exact for magnitudes from 2^-21 to 2^12 (8 significant bits above the last
+// FP16 bit, 2^-24).  If a pass holds others, its rows are read again, each with a power of two of
+// its own (largest exponent to 2^14): exact for elements down to 2^-31 of the row's largest.  If
+// a row spans more, or holds a NaN, an Inf or a BF16 subnormal, the pass uses BF16 operands
+// (kWide: the same codes, converted once more), which is exact for every input.
 #pragma once
 
 #include <cstdint>
 
+#include "nv4_async.cuh"
 #include "nv4_common.cuh"
 
 namespace nv4 {
@@ -28,44 +36,99 @@ namespace w4 {
 constexpr int kThreads = 512;                     // 16 warps, one CTA per SM
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kChunk = 256;                  // K-elements of one warp step
+constexpr int kDepth = 3;                         // chunks in flight per warp
+constexpr uint32_t kSlot = 16u * 128u + 16u * 16u;          // codes and scales of 16 rows x 256
+constexpr uint32_t kRing = kWarps * kDepth * kSlot;         // bytes for all warps
 
-struct Frag {
-    uint32_t q0[8], q1[8];                        // 64 codes of row g, of row g + 8
-    uint32_t s0, s1;                              // their 4 block scales (E4M3 bytes)
-};
-
-// 64 codes and 4 scales of one weight row from element k0 on; zeros where the row ends or is
-// not live.  kVec: K a multiple of 64 and 32-byte aligned rows (one 32-byte load).
-template <bool kVec>
-__device__ __forceinline__ void load_row(uint32_t (&q)[8], uint32_t& s, const uint8_t* __restrict__ qrow,
-                                         const uint8_t* __restrict__ srow, uint32_t k0, uint32_t K, bool live)
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live)
 {
-    if constexpr (kVec) {
-        if (live && k0 < K) {
-            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]),
-                           "=r"(q[7])
-                         : "l"(qrow + (k0 >> 1)));
-            s = __ldg(reinterpret_cast<const uint32_t*>(srow + (k0 >> 4)));
+    // no byte is read and zeros are written where it is not live
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(live ? kBytes : 0)
+                     : "memory");
+}
+
+// Starts the loads of chunk c of 16 weight rows into a ring slot: this lane's share of rows g and
+// g + 8 (qa, sa; qb, sb: where the rows' codes and scales begin; la, lb: whether they exist).
+// Slot: four 16-byte vectors per lane (row g halves 0 and 1, row g + 8 halves 0 and 1), then the
+// scales, 16 bytes per row.  kVec: K a multiple of 64 and 4-byte aligned scales; else 8 bytes of
+// codes at a time, scales byte by byte through registers.
+template <bool kVec>
+__device__ __forceinline__ void load_chunk(uint8_t* slot, const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
+                                           const uint8_t* sb, uint32_t c, uint32_t K, bool la, bool lb)
+{
+    const uint32_t lane = threadIdx.x & 31u, t = lane & 3u;
+    const uint32_t dst = smem_u32(slot) + 16u * lane, ks = c * kChunk + 64u * t;
+#pragma unroll
+    for (uint32_t p = 0; p < 2; ++p) {
+        const uint32_t k = c * kChunk + 128u * p + 32u * t;
+        if constexpr (kVec) {
+            cp_async<16>(dst + 512u * p, qa + k / 2u, la && k < K);
+            cp_async<16>(dst + 1024u + 512u * p, qb + k / 2u, lb && k < K);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = 0u;
-            s = 0u;
-        }
-    } else {
-        s = 0u;
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-            uint2 v = make_uint2(0u, 0u);
-            if (live && k0 + 16u * j < K) {
-                v = __ldg(reinterpret_cast<const uint2*>(qrow + (k0 >> 1) + 8u * j));
-                s |= (uint32_t)__ldg(srow + (k0 >> 4) + j) << (8u * j);
+            for (uint32_t j = 0; j < 2; ++j) {
+                cp_async<8>(dst + 512u * p + 8u * j, qa + k / 2u + 8u * j, la && k + 16u * j < K);
+                cp_async<8>(dst + 1024u + 512u * p + 8u * j, qb + k / 2u + 8u * j, lb && k + 16u * j < K);
             }
-            q[2 * j] = v.x;
-            q[2 * j + 1] = v.y;
         }
     }
+    const uint32_t sdst = smem_u32(slot) + 2048u + 4u * lane;      // row g = lane / 4, word t
+    if constexpr (kVec) {
+        cp_async<4>(sdst, sa + ks / 16u, la && ks < K);
+        cp_async<4>(sdst + 128u, sb + ks / 16u, lb && ks < K);
+    } else {
+        uint32_t a = 0u, b = 0u;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            if (la && ks + 16u * j < K) a |= (uint32_t)__ldg(sa + ks / 16u + j) << (8u * j);
+            if (lb && ks + 16u * j < K) b |= (uint32_t)__ldg(sb + ks / 16u + j) << (8u * j);
+        }
+        *reinterpret_cast<uint32_t*>(slot + 2048u + 4u * lane) = a;
+        *reinterpret_cast<uint32_t*>(slot + 2048u + 128u + 4u * lane) = b;
+    }
 }
+
+// Walks a warp's steps: load(slot) starts the next step's loads, use(slot) multiplies the next
+// one.  begin() before the token rows are staged, run() after.
+struct Ring {
+    uint8_t* base;                                // this warp's kDepth slots
+    uint32_t steps, issued;
+
+    template <class Load>
+    __device__ __forceinline__ void begin(uint8_t* b, uint32_t n, Load& load)
+    {
+        base = b;
+        steps = n;
+        issued = 0u;
+        for (int i = 0; i < kDepth; ++i) {
+            if (issued < steps) load(base + issued * kSlot);
+            ++issued;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+
+    template <class Load, class Use>
+    __device__ __forceinline__ void run(Load& load, Use use)
+    {
+        uint32_t at = 0u;
+        for (uint32_t i = 0; i < steps; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            __syncwarp();
+            uint8_t* slot = base + at * kSlot;
+            use(slot);
+            __syncwarp();                         // the slot has been read
+            if (issued < steps) load(slot);
+            ++issued;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            at = at + 1u == (uint32_t)kDepth ? 0u : at + 1u;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+};
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
@@ -84,16 +147,13 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h)
     return r;
 }
 
-// Four E4M3 scale bytes as FP16, each in both halves of a word.
-__device__ __forceinline__ void scale_pairs(uint32_t s, uint32_t (&p)[4])
+// Two E4M3 scale bytes as FP16, each in both halves of a word.
+__device__ __forceinline__ void scale_pair(uint16_t s, uint32_t (&p)[2])
 {
-    uint32_t a, b;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(s & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(s >> 16)));
+    uint32_t a;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"(s));
     p[0] = __byte_perm(a, a, 0x1010);
     p[1] = __byte_perm(a, a, 0x3232);
-    p[2] = __byte_perm(b, b, 0x1010);
-    p[3] = __byte_perm(b, b, 0x3232);
 }
 
 template <bool kWide>
@@ -112,37 +172,79 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// acc += 16 weight rows x m token rows over one chunk.  xs: the chunk's token values,
-// [8][m][4] 16-byte vectors: vector (u, token, t) holds elements 64 t + 8 u .. + 7.
-template <bool kWide, int NT>
-__device__ __forceinline__ void mma_chunk(float (&acc)[NT][4], const Frag& f, const uint4* xs, uint32_t m,
-                                          uint32_t g, uint32_t t)
+// Independent accumulators per 8-token tile: an MMA waits for the one before it on the same
+// accumulator, and with one chain of 16 per chunk that latency, not the decoding, set the pace
+// (156 clocks per chunk and SM with one chain, T = 5, K = 16384).
+template <int NT>
+constexpr int kChains = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+
+template <int NT>
+using Acc = float[kChains<NT>][NT][4];
+
+// acc += 16 weight rows x token rows over one chunk.  x(j, u): this lane's 16-byte vector of token
+// 8 j + g, the 8 elements from 128 (u / 4) + 32 t + 8 (u % 4) of the chunk on.
+template <bool kWide, int NT, class X>
+__device__ __forceinline__ void mma_step(Acc<NT>& acc, const uint8_t* slot, X x)
 {
-    uint32_t p0[4], p1[4];
-    scale_pairs(f.s0, p0);
-    scale_pairs(f.s1, p1);
+    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
 #pragma unroll
-    for (uint32_t u = 0; u < 8; ++u) {
-        uint32_t a[4], b[4];
-        cvt_e2m1x8_to_f16x8(f.q0[u], a);
-        cvt_e2m1x8_to_f16x8(f.q1[u], b);
+    for (uint32_t p = 0; p < 2; ++p) {
+        const uint4 qa = *reinterpret_cast<const uint4*>(slot + 512u * p + 16u * lane);
+        const uint4 qb = *reinterpret_cast<const uint4*>(slot + 1024u + 512u * p + 16u * lane);
+        uint32_t s0[2], s1[2];
+        scale_pair(*reinterpret_cast<const uint16_t*>(slot + 2048u + 16u * g + 8u * p + 2u * t), s0);
+        scale_pair(*reinterpret_cast<const uint16_t*>(slot + 2048u + 128u + 16u * g + 8u * p + 2u * t), s1);
+        const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = mul_f16x2(a[i], p0[u >> 1]);
-            b[i] = mul_f16x2(b[i], p1[u >> 1]);
-            if constexpr (kWide) {
-                a[i] = f16x2_to_bf16x2(a[i]);
-                b[i] = f16x2_to_bf16x2(b[i]);
+        for (uint32_t u = 0; u < 4; ++u) {
+            uint32_t a[4], b[4];
+            cvt_e2m1x8_to_f16x8(wa[u], a);
+            cvt_e2m1x8_to_f16x8(wb[u], b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = mul_f16x2(a[i], s0[u >> 1]);
+                b[i] = mul_f16x2(b[i], s1[u >> 1]);
+                if constexpr (kWide) {
+                    a[i] = f16x2_to_bf16x2(a[i]);
+                    b[i] = f16x2_to_bf16x2(b[i]);
+                }
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < (uint32_t)NT; ++j) {
+                const uint4 v = x(j, 4u * p + u);
+                mma<kWide>(acc[(2u * u) % kChains<NT>][j], a[0], b[0], a[1], b[1], v.x, v.y);
+                mma<kWide>(acc[(2u * u + 1u) % kChains<NT>][j], a[2], b[2], a[3], b[3], v.z, v.w);
             }
         }
-#pragma unroll
-        for (uint32_t j = 0; j < (uint32_t)NT; ++j) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (8u * j + g < m) x = xs[(u * m + 8u * j + g) * 4u + t];
-            mma<kWide>(acc[j], a[0], b[0], a[1], b[1], x.x, x.y);
-            mma<kWide>(acc[j], a[2], b[2], a[3], b[3], x.z, x.w);
-        }
     }
+}
+
+// Token rows in shared memory, xs: the chunk's [8][m][4] vectors (u, token, t).  Columns past m
+// are given token 0's values: nothing reads what they add up to.
+template <bool kWide, int NT>
+__device__ __forceinline__ void mma_chunk(Acc<NT>& acc, const uint8_t* slot, const uint4* xs, uint32_t m)
+{
+    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+    const uint4* x0[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x0[j] = xs + (8u * j + g < m ? 8u * j + g : 0u) * 4u + t;
+    mma_step<kWide, NT>(acc, slot, [&](uint32_t j, uint32_t u) { return x0[j][u * m * 4u]; });
+}
+
+// Up to 8 token rows in global memory, row: this lane's (column g's), K elements of it, k0: where
+// the chunk begins.
+template <bool kWide>
+__device__ __forceinline__ void mma_chunk_global(Acc<1>& acc, const uint8_t* slot, const uint16_t* row, uint32_t k0,
+                                                 uint32_t K)
+{
+    const uint32_t k = k0 + 32u * (threadIdx.x & 3u);
+    uint4 v[8];
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u) {
+        const uint32_t at = k + 128u * (u >> 2) + 8u * (u & 3u);
+        v[u] = at < K ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    mma_step<kWide, 1>(acc, slot, [&](uint32_t, uint32_t u) { return v[u]; });
 }
 
 // ---------------------------------------------------------------- token rows into shared memory
@@ -159,87 +261,134 @@ __device__ __forceinline__ float exp_field(int e)
     return e <= 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(e > 254 ? 254 : e) << 23);
 }
 
+// Where the 8 values from 8 l on of chunk c of token i of m go.
+__device__ __forceinline__ uint32_t vec_at(uint32_t c, uint32_t l, uint32_t m, uint32_t i)
+{
+    return ((c * 8u + 4u * (l >> 4) + (l & 3u)) * m + i) * 4u + ((l & 15u) >> 2);
+}
+
 // Converts m token rows (row(i): pointer to K values of the input type, 16-byte aligned) into
 // xs, [chunk][8][m][4] vectors, zero-padded to whole chunks.  kDt 0: BF16, 1: FP16.  Returns
 // (to every thread) whether the pass has to use BF16 operands.  All threads take part; ends
-// with a CTA barrier.
+// with a CTA barrier.  A warp takes one chunk of one token at a time.
 template <int kDt, class RowPtr>
 __device__ __forceinline__ bool stage_tokens(uint4* xs, Rows& rows, uint32_t m, uint32_t K, RowPtr row)
 {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-    const uint32_t nch = (K + kChunk - 1u) / kChunk, n = m * nch;
-    bool wide = false;
-    if constexpr (kDt == 0) {
-        if (threadIdx.x < m) {
-            rows.emax[threadIdx.x] = 0u;
-            rows.emin[threadIdx.x] = 0xFFFFu;
-        }
-        __syncthreads();
-        for (uint32_t it = warp; it < n; it += kWarps) {
-            const uint32_t i = it / nch, k = (it - i * nch) * kChunk + 8u * lane;
-            uint32_t hi = 0u, lo = 0xFFFFFFFFu;
-            if (k < K) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row(i)) + k));
-                const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+    const uint32_t nch = (K + kChunk - 1u) / kChunk;
+    auto fetch = [&](uint32_t i, uint32_t c) {
+        const uint32_t k = c * kChunk + 8u * lane;
+        return k < K ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row(i)) + k))
+                     : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto put = [&](uint32_t i, uint32_t c, uint4 v, bool convert, float f) {
+        if (convert) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hi = __vmaxu2(hi, w[j]);
-                    lo = __vminu2(lo, __vsub2(w[j], 0x00010001u));    // zero becomes 0xFFFF
-                }
-            }
-            hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16));
-            lo = __reduce_min_sync(0xFFFFFFFFu, min(lo & 0xFFFFu, lo >> 16));
-            if (lane == 0) {
-                atomicMax(&rows.emax[i], hi);
-                atomicMin(&rows.emin[i], lo);
-            }
+            for (int j = 0; j < 4; ++j)
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                    : "=r"(w[j])
+                    : "f"(__fmul_rn(bf16_hi(w[j]), f)), "f"(__fmul_rn(bf16_lo(w[j]), f)));
         }
-        __syncthreads();
-        bool mine = false;
-        if (threadIdx.x < m && rows.emax[threadIdx.x] != 0u) {
-            const int e1 = (int)(rows.emax[threadIdx.x] >> 7), e0 = (int)((rows.emin[threadIdx.x] + 1u) >> 7);
-            mine = e1 == 255 || e0 == 0 || e1 - e0 > 31 || e1 < 20;
-        }
-        wide = __syncthreads_or(mine) != 0;
-        if (threadIdx.x < m) {
-            const int e1 = (int)(rows.emax[threadIdx.x] >> 7);
-            rows.descale[threadIdx.x] = wide || e1 == 0 ? 1.0f : exp_field(e1 - 14);
-        }
-    } else {
-        if (threadIdx.x < m) rows.descale[threadIdx.x] = 1.0f;
-    }
-    for (uint32_t it = warp; it < n; it += kWarps) {
-        const uint32_t i = it / nch, c = it - i * nch, k = c * kChunk + 8u * lane;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (k < K) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row(i)) + k));
-        if constexpr (kDt == 0) {
-            if (!wide) {
-                const int e1 = (int)(rows.emax[i] >> 7);
-                const float f = e1 == 0 ? 1.0f : exp_field(268 - e1);
-                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        xs[vec_at(c, lane, m, i)] = v;
+    };
+    // magnitudes of 8 values: the largest, and the smallest non-zero one less one
+    auto scan = [&](const uint4& v, uint32_t& hi, uint32_t& lo) {
+        const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                        : "=r"(w[j])
-                        : "f"(__fmul_rn(bf16_hi(w[j]), f)), "f"(__fmul_rn(bf16_lo(w[j]), f)));
-            }
+        for (int j = 0; j < 4; ++j) {
+            hi = __vmaxu2(hi, w[j]);
+            lo = __vminu2(lo, __vsub2(w[j], 0x00010001u));        // zero becomes 0xFFFF
         }
-        xs[((c * 8u + (lane & 7u)) * m + i) * 4u + (lane >> 3)] = v;
+    };
+    // warp w takes steps w, w + 16, ... of the m x nch (token, chunk) pairs, token outermost, four
+    // loads at a time
+    auto each = [&](auto&& body) {
+        uint32_t i = 0u, c = warp;
+        auto settle = [&]() {
+            while (c >= nch && i < m) {
+                c -= nch;
+                ++i;
+            }
+        };
+        settle();
+        while (i < m) {
+            uint32_t is[4], cs[4];
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                is[j] = i;
+                cs[j] = c;
+                v[j] = i < m ? fetch(i, c) : make_uint4(0u, 0u, 0u, 0u);
+                c += kWarps;
+                settle();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (is[j] < m) body(is[j], cs[j], v[j]);
+        }
+    };
+    if (threadIdx.x < m) rows.descale[threadIdx.x] = kDt == 0 ? 0x1p-4f : 1.0f;
+    if constexpr (kDt == 1) {
+        each([&](uint32_t i, uint32_t c, const uint4& v) { put(i, c, v, false, 1.0f); });
+        __syncthreads();
+        return false;
     }
+    uint32_t hi = 0u, lo = 0xFFFFFFFFu;
+    each([&](uint32_t i, uint32_t c, const uint4& v) {
+        scan(v, hi, lo);
+        put(i, c, v, true, 0x1p4f);
+    });
+    // BF16 magnitudes 2^-21 = 0x3500 to below 2^12 = 0x4580, or zero
+    if (__syncthreads_or(max(hi & 0xFFFFu, hi >> 16) >= 0x4580u || min(lo & 0xFFFFu, lo >> 16) + 1u < 0x3500u) == 0)
+        return false;
+    // rows by their own exponents
+    if (threadIdx.x < m) {
+        rows.emax[threadIdx.x] = 0u;
+        rows.emin[threadIdx.x] = 0xFFFFu;
+    }
+    __syncthreads();
+    each([&](uint32_t i, uint32_t, const uint4& v) {
+        hi = 0u;
+        lo = 0xFFFFFFFFu;
+        scan(v, hi, lo);
+        hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16));
+        lo = __reduce_min_sync(0xFFFFFFFFu, min(lo & 0xFFFFu, lo >> 16));
+        if (lane == 0) {
+            atomicMax(&rows.emax[i], hi);
+            atomicMin(&rows.emin[i], lo);
+        }
+    });
+    __syncthreads();
+    bool mine = false;
+    if (threadIdx.x < m && rows.emax[threadIdx.x] != 0u) {
+        const int e1 = (int)(rows.emax[threadIdx.x] >> 7), e0 = (int)((rows.emin[threadIdx.x] + 1u) >> 7);
+        mine = e1 == 255 || e0 == 0 || e1 - e0 > 31 || e1 < 20;
+    }
+    const bool wide = __syncthreads_or(mine) != 0;
+    if (threadIdx.x < m) {
+        const int e1 = (int)(rows.emax[threadIdx.x] >> 7);
+        rows.descale[threadIdx.x] = wide || e1 == 0 ? 1.0f : exp_field(e1 - 14);
+    }
+    each([&](uint32_t i, uint32_t c, const uint4& v) {
+        const int e1 = (int)(rows.emax[i] >> 7);
+        put(i, c, v, !wide, e1 == 0 ? 1.0f : exp_field(268 - e1));
+    });
     __syncthreads();
     return wide;
 }
 
-// How many warps share a tile (its K range split between them): the power of two that gives
-// the shortest longest warp for ntile tiles of nch chunks on 16 warps; the smaller one of equals
-// (fewer partial sums to add).
-__device__ __forceinline__ uint32_t split_of(uint32_t ntile, uint32_t nch)
+// How many warps share a tile (its K range split between them): the power of two with the
+// shortest longest warp for ntile tiles of nch chunks on 16 warps, a tile's end and its barrier
+// counted as a quarter of a chunk's time.
+__host__ __device__ __forceinline__ uint32_t split_of(uint32_t ntile, uint32_t nch)
 {
     uint32_t best = 1u, cost = 0xFFFFFFFFu;
-    for (uint32_t wk = 1u; wk <= (uint32_t)kWarps && (wk == 1u || wk <= nch); wk *= 2u) {
-        const uint32_t groups = kWarps / wk;
-        const uint32_t c = ((ntile + groups - 1u) / groups) * ((nch + wk - 1u) / wk);
-        if (c < cost) {
+#pragma unroll
+    for (uint32_t lg = 0u; lg <= 4u; ++lg) {
+        const uint32_t wk = 1u << lg, groups = (uint32_t)kWarps >> lg;
+        const uint32_t c = ((ntile + groups - 1u) >> (4u - lg)) * (((nch + wk - 1u) >> lg) * 8u + (lg > 0u ? 2u : 1u));
+        if (c < cost && (lg == 0u || wk <= nch)) {
             cost = c;
             best = wk;
         }
@@ -247,10 +396,63 @@ __device__ __forceinline__ uint32_t split_of(uint32_t ntile, uint32_t nch)
     return best;
 }
 
-__device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads)
+// Barrier of the wk warps of a group (at most 8 groups of more than one warp: barriers 1-8).
+__device__ __forceinline__ void group_barrier(uint32_t grp, uint32_t wk)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+    if (wk == 1u) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1u + grp), "r"(32u * wk) : "memory");
 }
+
+// Adds wk partial sums, kTile apart, in warp order.
+template <uint32_t kTile>
+__device__ __forceinline__ float sum_parts(const float* first, uint32_t wk)
+{
+    float s = 0.0f;
+#pragma unroll 4
+    for (uint32_t w = 0; w < wk; ++w) s += first[(size_t)w * kTile];
+    return s;
+}
+
+template <int NT>
+__device__ __forceinline__ void clear(Acc<NT>& acc)
+{
+#pragma unroll
+    for (int c = 0; c < kChains<NT>; ++c)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[c][j][0] = acc[c][j][1] = acc[c][j][2] = acc[c][j][3] = 0.0f;
+}
+
+// The chains' sum, in chain (0).
+template <int NT>
+__device__ __forceinline__ void join(Acc<NT>& acc)
+{
+#pragma unroll
+    for (int c = kChains<NT> / 2; c > 0; c /= 2)
+#pragma unroll
+        for (int i = 0; i < c; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] += acc[i + c][j][v];
+}
+
+// A warp's 16 x 8 NT sums to its place in shared memory, [16][8 NT].
+template <int NT>
+__device__ __forceinline__ void put_part(float* part, Acc<NT>& chains, uint32_t g, uint32_t t)
+{
+    join<NT>(chains);
+    const float (&acc)[NT][4] = chains[0];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        *reinterpret_cast<float2*>(part + g * (8 * NT) + 8 * j + 2 * t) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(part + (g + 8) * (8 * NT) + 8 * j + 2 * t) = make_float2(acc[j][2], acc[j][3]);
+    }
+}
+
+// Programmatic dependent launch: wait for the kernel before (its writes are visible then); let
+// the kernel behind start its own prologue.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <int kOut>
 __device__ __forceinline__ void store_out(void* out, int64_t at, float v)

@@ -4,12 +4,13 @@
 // code is e2m1 * s_b * s2).  y[t, n] = s2 * sum_k x[t, k] * (e2m1(q[n, k]) * e4m3(s[n, k/16])):
 // the weight products are exact, the sum runs in FP32, s2 is applied to the sum.
 //
-// One persistent CTA per SM owns a contiguous range of weight rows (balanced to one row) and
-// walks it in tiles of at most 16 rows; its 16 warps split a tile's K range (nv4_w4.cuh), so a
-// weight byte is read once per pass of up to 24 tokens.  Token rows are staged once per pass.
+// One CTA per SM; a cluster of z of them owns a contiguous range of weight rows (balanced to one
+// row) and splits K, each CTA taking its chunks of it: staging the token rows costs a CTA
+// T * K / z values, so z grows with T * K.  A CTA walks its rows in tiles of at most 16; its 16
+// warps split the tiles and, within a tile, K (nv4_w4.cuh).  A weight byte is read once per pass of up to 24 tokens.  The cluster's partial sums
+// meet through distributed shared memory, added in rank order.
+#include "nv4_async.cuh"
 #include "nv4_internal.h"
-#include <type_traits>
-
 #include "nv4_w4.cuh"
 
 namespace nv4 {
@@ -25,6 +26,8 @@ struct LinearParams {
     void* out;
     int64_t ldd;
     uint32_t T, N, K, cap;                        // cap: tokens per pass
+    uint32_t z, xs_bytes, red_bytes;              // cluster size; shared memory of token rows, of warp sums
+    uint32_t tile, ntile, wk;                     // rows per tile, tiles per cluster, warps per tile
 };
 
 template <int kDt, int kOut, bool kVec, int NT>
@@ -33,81 +36,157 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Rows rows;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
-    const uint32_t nch = (p.K + kChunk - 1u) / kChunk;
-    uint4* xs = reinterpret_cast<uint4*>(smem);
-    float* red = reinterpret_cast<float*>(smem + (size_t)nch * 512u * p.cap);     // [2][16 warps][16][8 NT]
+    uint4* xs = reinterpret_cast<uint4*>(smem + kRing);
+    float* red = reinterpret_cast<float*>(smem + kRing + p.xs_bytes);          // [2][16 warps][16][8 NT]
+    float* part = red + p.red_bytes / sizeof(float);                           // [rows][8 NT], z > 1
     constexpr uint32_t kTile = 16u * 8u * NT;
-    const uint32_t r0 = (uint32_t)((uint64_t)blockIdx.x * p.N / gridDim.x);
-    const uint32_t R = (uint32_t)((uint64_t)(blockIdx.x + 1u) * p.N / gridDim.x) - r0;
-    const uint32_t ntile = (R + 15u) / 16u;
-    const uint32_t wk = split_of(ntile, nch), groups = kWarps / wk;
+    const uint32_t rank = p.z > 1u ? cluster_ctarank() : 0u;
+    const uint32_t clu = blockIdx.x / p.z, nclu = gridDim.x / p.z;
+    const uint32_t r0 = (uint32_t)((uint64_t)clu * p.N / nclu);
+    const uint32_t R = (uint32_t)((uint64_t)(clu + 1u) * p.N / nclu) - r0, ntile = p.ntile;
+    const uint32_t all = (p.K + kChunk - 1u) / kChunk;
+    const uint32_t ch0 = rank * all / p.z, nch = (rank + 1u) * all / p.z - ch0;
+    const uint32_t kb = ch0 * kChunk, kn = min(p.K, kb + nch * kChunk) - kb;   // this CTA's K range
+    const uint32_t wk = p.wk, groups = kWarps / wk;
     const uint32_t grp = warp / wk, wig = warp - grp * wk;
     const float s2 = *p.d_s2;
-
-    auto load = [&](Frag& f, uint32_t tile, uint32_t c) {
-        const uint32_t a = r0 + tile * R / ntile, b = r0 + (tile + 1u) * R / ntile;
-        const uint32_t k0 = c * kChunk + 64u * t, ra = a + g, rb = a + 8u + g;
-        load_row<kVec>(f.q0, f.s0, p.q + (size_t)ra * (p.K / 2u), p.sc + (size_t)ra * (p.K / 16u), k0, p.K, ra < b);
-        load_row<kVec>(f.q1, f.s1, p.q + (size_t)rb * (p.K / 2u), p.sc + (size_t)rb * (p.K / 16u), k0, p.K, rb < b);
-    };
+    const uint32_t my_tiles = grp < ntile ? (ntile - grp + groups - 1u) / groups : 0u;
+    const uint32_t my_chunks = wig < nch ? (nch - wig + wk - 1u) / wk : 0u, steps = my_tiles * my_chunks;
 
     for (uint32_t p0 = 0; p0 < p.T; p0 += p.cap) {
         const uint32_t m = min(p.cap, p.T - p0);
-        Frag cur;
-        if (grp < ntile) load(cur, grp, wig);     // in flight while the tokens are staged
+        uint32_t lt = grp, lc = wig;              // the step to load next
+        size_t row = 0;                           // byte offset of row g's codes of the tile to load
+        bool la = false, lb = false, moved = true;
+        auto load = [&](uint8_t* slot) {
+            if (moved) {
+                const uint32_t a = r0 + lt * p.tile, n = min(p.tile, r0 + R - min(a, r0 + R));
+                row = (size_t)(a + g) * (p.K / 2u);
+                la = g < n;
+                lb = g + 8u < n;
+                moved = false;
+            }
+            const size_t row8 = row + (size_t)8u * (p.K / 2u);
+            load_chunk<kVec>(slot, p.q + row, p.sc + row / 8u, p.q + row8, p.sc + row8 / 8u, ch0 + lc, p.K, la, lb);
+            lc += wk;
+            if (lc >= nch) {
+                lc = wig;
+                lt += groups;
+                moved = true;
+            }
+        };
+        Ring ring;
+        ring.begin(smem + warp * (kDepth * kSlot), steps, load);
         if (p0 > 0) __syncthreads();              // the previous pass has read its tokens
-        const bool wide = stage_tokens<kDt>(xs, rows, m, p.K, [&](uint32_t i) {
-            return static_cast<const void*>(static_cast<const uint16_t*>(p.x) + (int64_t)(p0 + i) * p.ldx);
+        const bool wide = stage_tokens<kDt>(xs, rows, m, kn, [&](uint32_t i) {
+            return static_cast<const void*>(static_cast<const uint16_t*>(p.x) + (int64_t)(p0 + i) * p.ldx + kb);
         });
-        uint32_t buf = 0u;
-        for (uint32_t tile = grp; tile < ntile; tile += groups, buf ^= 1u) {
-            float acc[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-            for (uint32_t c = wig; c < nch; c += wk) {
-                Frag next;
-                const bool more = c + wk < nch;
-                if (more || tile + groups < ntile) load(next, more ? tile : tile + groups, more ? c + wk : wig);
-                const uint4* xc = xs + (size_t)c * 32u * m;
-                if (kDt == 0 && wide)
-                    mma_chunk<true, NT>(acc, cur, xc, m, g, t);
-                else
-                    mma_chunk<false, NT>(acc, cur, xc, m, g, t);
-                cur = next;
-            }
-            float* part = red + (size_t)(buf * kWarps + warp) * kTile;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                *reinterpret_cast<float2*>(part + g * (8 * NT) + 8 * j + 2 * t) = make_float2(acc[j][0], acc[j][1]);
-                *reinterpret_cast<float2*>(part + (g + 8) * (8 * NT) + 8 * j + 2 * t) = make_float2(acc[j][2], acc[j][3]);
-            }
-            if (wk == 1u) __syncwarp();
-            else group_barrier(1u + grp, 32u * wk);           // at most 8 groups: barriers 1-8
-            // the group adds its warps' partial sums, one (token, row) per thread, in warp order
-            const uint32_t a = r0 + tile * R / ntile, nr = r0 + (tile + 1u) * R / ntile - a;
+        Acc<NT> acc;
+        clear<NT>(acc);
+        uint32_t ut = grp, uc = wig, buf = 0u;    // the step to multiply next
+        ring.run(load, [&](const uint8_t* slot) {
+            const uint4* xc = xs + (size_t)uc * 32u * m;
+            if (kDt == 0 && wide) mma_chunk<true, NT>(acc, slot, xc, m);
+            else mma_chunk<false, NT>(acc, slot, xc, m);
+            uc += wk;
+            if (uc < nch) return;
+            // the tile's end: the group adds its warps' sums, one (token, row) per thread
+            put_part<NT>(red + (size_t)(buf * kWarps + warp) * kTile, acc, g, t);
+            clear<NT>(acc);
+            group_barrier(grp, wk);
+            const uint32_t a = ut * p.tile, nr = a < R ? min(p.tile, R - a) : 0u;
             const float* first = red + (size_t)(buf * kWarps + grp * wk) * kTile;
             for (uint32_t i = wig * 32u + lane; i < 16u * m; i += 32u * wk) {
                 const uint32_t r = i & 15u, tok = i >> 4;
                 if (r >= nr) continue;
-                float s = 0.0f;
-                for (uint32_t w = 0; w < wk; ++w) s += first[(size_t)w * kTile + r * (8 * NT) + tok];
-                store_out<kOut>(p.out, (int64_t)(p0 + tok) * p.ldd + a + r, s * s2 * rows.descale[tok]);
+                const float s = sum_parts<kTile>(first + r * (8 * NT) + tok, wk);
+                if (p.z > 1u) part[(size_t)(a + r) * (8 * NT) + tok] = s * rows.descale[tok];
+                else store_out<kOut>(p.out, (int64_t)(p0 + tok) * p.ldd + r0 + a + r, s * s2 * rows.descale[tok]);
             }
+            buf ^= 1u;
+            uc = wig;
+            ut += groups;
+        });
+        if (p.z > 1u) {
+            cluster_sync();
+            const uint32_t n = R * m, i1 = (uint32_t)((uint64_t)(rank + 1u) * n / p.z);
+            for (uint32_t i = (uint32_t)((uint64_t)rank * n / p.z) + threadIdx.x; i < i1; i += kThreads) {
+                const uint32_t tok = i / R, r = i - tok * R;
+                float v[8], s = 0.0f;
+#pragma unroll
+                for (uint32_t q = 0; q < 8u; ++q) v[q] = q < p.z ? ld_dsmem_f32(part + (size_t)r * (8 * NT) + tok, q) : 0.0f;
+#pragma unroll
+                for (uint32_t q = 0; q < 8u; ++q) s += v[q];
+                store_out<kOut>(p.out, (int64_t)(p0 + tok) * p.ldd + r0 + r, s * s2);
+            }
+            cluster_sync();                       // the others' sums have been read
         }
     }
 }
 
-template <int kDt, int kOut, bool kVec>
-static cudaError_t run_linear(const LinearParams& p, uint32_t nt, cudaStream_t s)
+template <int kDt, int kOut, bool kVec, int NT>
+static cudaError_t run_linear(LinearParams p, cudaStream_t s)
 {
-    auto kern = nt == 1 ? linear_kernel<kDt, kOut, kVec, 1>
-                        : nt == 2 ? linear_kernel<kDt, kOut, kVec, 2> : linear_kernel<kDt, kOut, kVec, 3>;
-    const size_t smem = (size_t)((p.K + kChunk - 1u) / kChunk) * 512u * p.cap + 2u * kWarps * 16u * 8u * nt * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kern = linear_kernel<kDt, kOut, kVec, NT>;
+    static bool ready[64] = {};
+    static int fits[64][4] = {};                  // clusters of 1, 2, 4, 8 that run at once
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint32_t sms = (uint32_t)num_sms();
-    kern<<<p.N < sms ? p.N : sms, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    const bool known = dev >= 0 && dev < 64;
+    if (!known || !ready[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmemW4);
+        if (e != cudaSuccess) return e;
+        if (known) ready[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.z;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.z > 1u ? 1 : 0;
+    const int lg = p.z == 1u ? 0 : p.z == 2u ? 1 : p.z == 4u ? 2 : 3;
+    int n = known ? fits[dev][lg] : 0;
+    if (n <= 0) {
+        n = num_sms() / (int)p.z;
+        if (p.z > 1u) {
+            cfg.gridDim = dim3((uint32_t)n * p.z, 1, 1);
+            cfg.dynamicSmemBytes = kMaxSmemW4;
+            int m = 0;
+            if (cudaOccupancyMaxActiveClusters(&m, kern, &cfg) == cudaSuccess && m > 0) n = m < n ? m : n;
+            else (void)cudaGetLastError();
+        }
+        if (known) fits[dev][lg] = n;
+    }
+    p.red_bytes = 2u * kWarps * 16u * 8u * NT * (uint32_t)sizeof(float);
+    const size_t fixed = kRing + (size_t)p.xs_bytes + p.red_bytes;
+    uint32_t nclu = p.N < (uint32_t)n ? p.N : (uint32_t)n;
+    if (p.z > 1u) {                               // more clusters than run at once if their sums need it
+        const uint32_t fit = (uint32_t)((kMaxSmemW4 - fixed) / (8u * NT * sizeof(float)));
+        if ((p.N + fit - 1u) / fit > nclu) nclu = (p.N + fit - 1u) / fit;
+    }
+    const uint32_t most = (p.N + nclu - 1u) / nclu;
+    p.ntile = (most + 15u) / 16u;
+    p.tile = (most + p.ntile - 1u) / p.ntile;
+    p.wk = split_of(p.ntile, (p.K + kChunk - 1u) / kChunk / p.z);
+    const size_t smem = fixed + (p.z > 1u ? (size_t)most * 8u * NT * sizeof(float) : 0u);
+    cfg.gridDim = dim3(nclu * p.z, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int kDt, int kOut>
+static cudaError_t pick_linear(const LinearParams& p, bool vec, cudaStream_t s)
+{
+    const uint32_t nt = (p.cap + 7u) / 8u;
+    if (vec) return nt == 1 ? run_linear<kDt, kOut, true, 1>(p, s)
+                            : nt == 2 ? run_linear<kDt, kOut, true, 2>(p, s) : run_linear<kDt, kOut, true, 3>(p, s);
+    return nt == 1 ? run_linear<kDt, kOut, false, 1>(p, s)
+                   : nt == 2 ? run_linear<kDt, kOut, false, 2>(p, s) : run_linear<kDt, kOut, false, 3>(p, s);
 }
 
 }  // namespace w4
@@ -117,21 +196,22 @@ cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int
                                 cudaStream_t s)
 {
     using namespace w4;
-    LinearParams p{x, ldx, q, sc, d_s2, out, ldd, (uint32_t)T, (uint32_t)N, (uint32_t)K, 0u};
-    // tokens per pass: what shared memory holds beside the partial sums, 24 at most
-    const uint32_t per_token = (uint32_t)((K + kChunk - 1) / kChunk) * 512u;
-    uint32_t cap = (uint32_t)(T < 24 ? T : 24);
-    while (cap > 1u && (size_t)cap * per_token + 2u * kWarps * 128u * ((cap + 7u) / 8u) * sizeof(float) > kMaxSmemW4) --cap;
-    p.cap = cap;
-    const uint32_t nt = (cap + 7u) / 8u;
-    const bool vec = K % 64 == 0 && (reinterpret_cast<uintptr_t>(q) & 31u) == 0u && (reinterpret_cast<uintptr_t>(sc) & 3u) == 0u;
-    auto pick = [&](auto dt_c) {
-        constexpr int D = decltype(dt_c)::value;
-        if (out_dt == 0) return vec ? run_linear<D, 0, true>(p, nt, s) : run_linear<D, 0, false>(p, nt, s);
-        if (out_dt == 1) return vec ? run_linear<D, 1, true>(p, nt, s) : run_linear<D, 1, false>(p, nt, s);
-        return vec ? run_linear<D, 2, true>(p, nt, s) : run_linear<D, 2, false>(p, nt, s);
-    };
-    return dt == 0 ? pick(std::integral_constant<int, 0>{}) : pick(std::integral_constant<int, 1>{});
+    const uint32_t nch = (uint32_t)((K + kChunk - 1) / kChunk);
+    uint32_t cap = (uint32_t)(T < 24 ? T : 24), z = 1u;
+    // split K until a CTA stages 128 chunks of token rows, as long as it keeps two chunks of K;
+    // clusters of 8 leave a sixth of the SMs without one (15 fit at once), of 4 hardly any
+    while (z < 4u && cap * nch > 128u * z && nch >= 4u * z) z *= 2u;
+    const uint32_t per = (nch + z - 1u) / z * 512u;                // bytes of a token row in a CTA
+    // per 8 tokens: the warps' sums, twice, and a cluster's sums of at least 256 rows
+    const size_t sums = (2u * kWarps * 128u + 2048u) * sizeof(float);
+    while (cap > 1u && kRing + (size_t)cap * per + ((cap + 7u) / 8u) * sums > kMaxSmemW4) --cap;
+    const LinearParams p{x, ldx, q, sc, d_s2, out, ldd, (uint32_t)T, (uint32_t)N, (uint32_t)K, cap, z, cap * per, 0u, 0u, 0u, 0u};
+    const bool vec = K % 64 == 0;                                  // (the scales are 16-byte aligned)
+    if (dt == 0)
+        return out_dt == 0 ? pick_linear<0, 0>(p, vec, s)
+                           : out_dt == 1 ? pick_linear<0, 1>(p, vec, s) : pick_linear<0, 2>(p, vec, s);
+    return out_dt == 0 ? pick_linear<1, 0>(p, vec, s)
+                       : out_dt == 1 ? pick_linear<1, 1>(p, vec, s) : pick_linear<1, 2>(p, vec, s);
 }
 
 }  // namespace nv4

@@ -48,7 +48,7 @@ def check(orc, x, ids, weights, gate, up, down, out_dt="bf16", out=None):
     if out is None:
         out = nv4.moe_experts(x, di, dw, g, u, d, dtype=DT[out_dt], d_flags=f)
     else:
-        work = torch.full((ids.size * gate[0].shape[1],), float("nan"), device=G.DEV)
+        work = torch.full((nv4.nv4_moe_work_bytes(*ids.shape, x.shape[1], gate[0].shape[1]),), 0xFF, dtype=torch.uint8, device=G.DEV)
         nv4.nv4_moe_experts(x, di, dw, g, u, d, out, work, f)
     torch.cuda.synchronize()
     assert f.item() == 0
@@ -174,7 +174,7 @@ def test_layer_run(orc):
     xin, out = xs[0].clone(), torch.empty_like(want[0])
     ids = torch.empty((T, k), dtype=torch.int32, device=G.DEV)
     w = torch.empty((T, k), device=G.DEV)
-    work = torch.empty(nv4.nv4_moe_work_bytes(T, k, I), dtype=torch.uint8, device=G.DEV)
+    work = torch.empty(nv4.nv4_moe_work_bytes(T, k, H, I), dtype=torch.uint8, device=G.DEV)
     nv4.nv4_moe_layer(xin, wr, g, u, d, ids, w, out, work)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()

@@ -101,6 +101,14 @@ def test_linear_wide_rows(orc, T):
     check(orc, x.to(G.DEV), q, sc, 0.5, "fp32")
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** -18, 2.0 ** 9, 2.0 ** 30])
+def test_linear_rows_of_other_magnitudes(orc, scale):
+    """Rows outside the range that the first conversion holds exactly."""
+    rng = np.random.default_rng(8)
+    q, sc = weights(rng, 130, 608)
+    check(orc, (rows(rng, 5, 608, "bf16") * scale).to(G.DEV), q, sc, 0.125, "fp32")
+
+
 def test_linear_nonfinite_propagates(orc):
     rng = np.random.default_rng(5)
     q, sc = weights(rng, 40, 128)
