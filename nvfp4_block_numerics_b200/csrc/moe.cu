@@ -42,8 +42,9 @@ using w4::kWarps;
 constexpr uint32_t kPass = 8;                     // tokens of one expert multiplied at once
 
 // ---------------------------------------------------------------- token rows
-// The workspace: x as FP16 [T][H], what undoes each row's scaling (negative: the row is not held
-// by FP16, see w4::stage_tokens), h in FP32 [rows][I], h as FP16 [rows][I], its scales.
+// The workspace: x as FP16 in vector order [T][H padded], what undoes each row's scaling
+// (negative: the row is not held by FP16, see w4::stage_tokens), h in FP32 [rows][I], h as FP16 in
+// vector order [rows][I padded], its scales.
 struct Work {
     uint16_t* x16;
     float* xd;
@@ -64,62 +65,72 @@ __host__ inline Work work_of(void* w, size_t T, size_t k, size_t H, size_t I, si
         return r;
     };
     Work o;
-    o.x16 = reinterpret_cast<uint16_t*>(take(T * H * 2u));
+    o.x16 = reinterpret_cast<uint16_t*>(take(T * w4::padded((uint32_t)H) * 2u));
     o.xd = reinterpret_cast<float*>(take(T * 4u));
     o.h = reinterpret_cast<float*>(take(T * k * I * 4u));
-    o.h16 = reinterpret_cast<uint16_t*>(take(T * k * I * 2u));
+    o.h16 = reinterpret_cast<uint16_t*>(take(T * k * w4::padded((uint32_t)I) * 2u));
     o.hd = reinterpret_cast<float*>(take(T * k * 4u));
     *bytes = at;
     return o;
 }
 
-// The CTA's threads convert one BF16 row to FP16 with a power of two of its own.
+// The CTA's threads bring one row into vector order, a BF16 one (kDt 0) converted to FP16 with a
+// power of two of its own.
+template <int kDt>
 __device__ __forceinline__ void convert_row(const uint16_t* x, uint32_t H, uint16_t* out, float* descale, uint32_t* red)
 {
     const uint32_t tid = threadIdx.x, n = blockDim.x, warp = tid >> 5, lane = tid & 31u;
-    uint32_t hi = 0u, lo = 0xFFFFFFFFu;
-    for (uint32_t k = 8u * tid; k < H; k += 8u * n) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
-        const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+    float f = 1.0f;
+    if constexpr (kDt == 0) {
+        uint32_t hi = 0u, lo = 0xFFFFFFFFu;
+        for (uint32_t k = 8u * tid; k < H; k += 8u * n) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+            const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            hi = __vmaxu2(hi, w[j]);
-            lo = __vminu2(lo, __vsub2(w[j], 0x00010001u));        // zero becomes 0xFFFF
+            for (int j = 0; j < 4; ++j) {
+                hi = __vmaxu2(hi, w[j]);
+                lo = __vminu2(lo, __vsub2(w[j], 0x00010001u));    // zero becomes 0xFFFF
+            }
         }
+        hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16));
+        lo = __reduce_min_sync(0xFFFFFFFFu, min(lo & 0xFFFFu, lo >> 16));
+        if (lane == 0u) {
+            red[warp] = hi;
+            red[32u + warp] = lo;
+        }
+        __syncthreads();
+        for (uint32_t w = 0; w < n / 32u; ++w) {
+            hi = max(hi, red[w]);
+            lo = min(lo, red[32u + w]);
+        }
+        const int e1 = (int)(hi >> 7), e0 = (int)((lo + 1u) >> 7);
+        const bool wide = hi != 0u && (e1 == 255 || e0 == 0 || e1 - e0 > 31 || e1 < 20);
+        f = hi == 0u || wide ? 1.0f : w4::exp_field(268 - e1);
+        if (tid == 0u) *descale = wide ? -1.0f : hi == 0u ? 1.0f : w4::exp_field(e1 - 14);
+    } else {
+        if (tid == 0u) *descale = 1.0f;
     }
-    hi = __reduce_max_sync(0xFFFFFFFFu, max(hi & 0xFFFFu, hi >> 16));
-    lo = __reduce_min_sync(0xFFFFFFFFu, min(lo & 0xFFFFu, lo >> 16));
-    if (lane == 0u) {
-        red[warp] = hi;
-        red[32u + warp] = lo;
-    }
-    __syncthreads();
-    for (uint32_t w = 0; w < n / 32u; ++w) {
-        hi = max(hi, red[w]);
-        lo = min(lo, red[32u + w]);
-    }
-    const int e1 = (int)(hi >> 7), e0 = (int)((lo + 1u) >> 7);
-    const bool wide = hi != 0u && (e1 == 255 || e0 == 0 || e1 - e0 > 31 || e1 < 20);
-    const float f = hi == 0u || wide ? 1.0f : w4::exp_field(268 - e1);
-    if (tid == 0u) *descale = wide ? -1.0f : hi == 0u ? 1.0f : w4::exp_field(e1 - 14);
-    for (uint32_t k = 8u * tid; k < H; k += 8u * n) {
-        uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+    for (uint32_t i = tid; i < w4::padded(H) / 8u; i += n) {
+        uint4 v = 8u * i < H ? __ldg(reinterpret_cast<const uint4*>(x + 8u * i)) : make_uint4(0u, 0u, 0u, 0u);
         uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        if constexpr (kDt == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                : "=r"(w[j])
-                : "f"(__fmul_rn(bf16_hi(w[j]), f)), "f"(__fmul_rn(bf16_lo(w[j]), f)));
-        *reinterpret_cast<uint4*>(out + k) = v;
+            for (int j = 0; j < 4; ++j)
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                    : "=r"(w[j])
+                    : "f"(__fmul_rn(bf16_hi(w[j]), f)), "f"(__fmul_rn(bf16_lo(w[j]), f)));
+        }
+        *reinterpret_cast<uint4*>(out + w4::vec_offset(i)) = v;
     }
 }
 
+template <int kDt>
 __global__ void __launch_bounds__(512) moe_rows_kernel(const void* x, int64_t ldx, uint32_t H, Work w)
 {
     __shared__ uint32_t red[64];
     w4::pdl_launch();
-    convert_row(static_cast<const uint16_t*>(x) + (int64_t)blockIdx.x * ldx, H, w.x16 + (size_t)blockIdx.x * H,
-                w.xd + blockIdx.x, red);
+    convert_row<kDt>(static_cast<const uint16_t*>(x) + (int64_t)blockIdx.x * ldx, H,
+                     w.x16 + (size_t)blockIdx.x * w4::padded(H), w.xd + blockIdx.x, red);
 }
 
 // ---------------------------------------------------------------- router
@@ -212,10 +223,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
     if (!waited) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     __syncwarp();
     cluster_sync();
-    if (kDt == 0 && p.work.x16 != nullptr && rank >= kRouteTokens && rank - kRouteTokens < nt) {
+    if (p.work.x16 != nullptr && rank >= kRouteTokens && rank - kRouteTokens < nt) {
         __shared__ uint32_t red[64];
         const uint32_t i = rank - kRouteTokens;
-        convert_row(x + (int64_t)i * p.ldx, p.H, p.work.x16 + (size_t)(t0 + i) * p.H, p.work.xd + t0 + i, red);
+        convert_row<kDt>(x + (int64_t)i * p.ldx, p.H, p.work.x16 + (size_t)(t0 + i) * w4::padded(p.H), p.work.xd + t0 + i, red);
     }
     if (rank >= nt) return;
     const size_t row = (size_t)(t0 + rank) * p.k;
@@ -368,7 +379,7 @@ struct Segs {
     uint32_t n, ntile, pairs;
 };
 
-template <int kDt, bool kVec>
+template <bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ Experts p)
 {
     extern __shared__ __align__(16) uint8_t smem[];                // the warps' rings
@@ -381,13 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     const uint32_t nch = (p.H + kChunk - 1u) / kChunk;
     w4::pdl_wait();                                                // ids are the router's
     w4::pdl_launch();
-    // BF16 rows: their FP16 form, unless some row has none: then all as they are
-    float d = 1.0f;
-    if (kDt == 0 && tid < p.T) d = p.work.xd[tid];
+    // the rows in their FP16 form, unless some BF16 row has none: then all as they are
+    const float d = tid < p.T ? p.work.xd[tid] : 1.0f;
     const bool wide = __syncthreads_or(d < 0.0f) != 0;
     if (tid < p.T) descale[tid] = wide ? 1.0f : d;
-    const uint16_t* x = kDt == 1 || wide ? static_cast<const uint16_t*>(p.x) : p.work.x16;
-    const int64_t ldx = kDt == 1 || wide ? p.ldx : (int64_t)p.H;
+    const uint16_t* x = wide ? static_cast<const uint16_t*>(p.x) : p.work.x16;
+    const int64_t ldx = wide ? p.ldx : (int64_t)w4::padded(p.H);
     build_lists(L, p);
     const uint32_t total = L.subs * p.I;                           // at most 768 x 2^15
     uint32_t at = (uint32_t)((uint64_t)blockIdx.x * total / gridDim.x);
@@ -452,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
                 while (us + 1u < S.n && ut >= S.s[us + 1u].tile0) ++us;
                 xr = x + (int64_t)L.tok[S.s[us].f0 + min(g, S.s[us].m - 1u)] * ldx;
             }
-            if (kDt == 0 && wide) w4::mma_chunk_global<true>(acc, slot, xr, uc * kChunk, p.H);
-            else w4::mma_chunk_global<false>(acc, slot, xr, uc * kChunk, p.H);
+            if (wide) w4::mma_chunk_global<true>(acc, slot, xr, uc, p.H);
+            else w4::mma_chunk_global<false>(acc, slot, xr, uc, p.H);
             uc += wk;
             if (uc < nch) return;
             w4::put_part<1>(red[buf][warp], acc, g, t);
@@ -531,12 +541,14 @@ __global__ void __launch_bounds__(256) moe_hidden_kernel(const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(__fmul_rn(z[2 * j + 1], f)), "f"(__fmul_rn(z[2 * j], f)));
-        *reinterpret_cast<uint4*>(p.work.h16 + (size_t)blockIdx.x * p.I + 8u * v) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(p.work.h16 + (size_t)blockIdx.x * w4::padded(p.I) + w4::vec_offset(v)) = make_uint4(o[0], o[1], o[2], o[3]);
     };
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
-        if (8u * (tid + 256u * i) < p.I) put(tid + 256u * i, keep[i][0], keep[i][1]);
-    for (uint32_t v = tid + 256u * kKeep; 8u * v < p.I; v += 256u) put(v, src[2u * v], src[2u * v + 1u]);
+        if (8u * (tid + 256u * i) < w4::padded(p.I)) put(tid + 256u * i, keep[i][0], keep[i][1]);
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (uint32_t v = tid + 256u * kKeep; 8u * v < w4::padded(p.I); v += 256u)
+        put(v, 8u * v < p.I ? src[2u * v] : zero, 8u * v < p.I ? src[2u * v + 1u] : zero);
 }
 
 // ---------------------------------------------------------------- down, weighted sum
@@ -609,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             if (us >= L.sub[ua + 1u]) ++ua;
             f0 = L.first[ua] + (us - L.sub[ua]) * kPass;
             m = min(kPass, L.first[ua + 1u] - f0);
-            xr = p.work.h16 + (size_t)(f0 + min(g, m - 1u)) * p.I;
+            xr = p.work.h16 + (size_t)(f0 + min(g, m - 1u)) * w4::padded(p.I);
             fresh = false;
         }
-        w4::mma_chunk_global<false>(acc, slot, xr, uc * kChunk, p.I);
+        w4::mma_chunk_global<false>(acc, slot, xr, uc, p.I);
         --left;
         if (++uc < nch && left != 0u) return;
         // the sub-list's end: its columns, each times its coefficient, into the warp's sums
@@ -694,13 +706,13 @@ static cudaError_t run_route(const RouteParams& p, cudaStream_t s)
     return launch(moe_route_kernel<kDt, kTok>, p, (p.T + kTok - 1u) / kTok * kRouteCtas, kRouteThreads, 0, kRouteCtas, false, s);
 }
 
-template <int kDt, bool kVec>
-static cudaError_t run_up(const Experts& p, bool dependent, cudaStream_t s)
+template <bool kVec>
+static cudaError_t run_up(const Experts& p, cudaStream_t s)
 {
     static bool ready[64] = {};
-    const cudaError_t e = prepare(moe_up_kernel<kDt, kVec>, ready, (int)w4::kRing, false);
+    const cudaError_t e = prepare(moe_up_kernel<kVec>, ready, (int)w4::kRing, false);
     if (e != cudaSuccess) return e;
-    return launch(moe_up_kernel<kDt, kVec>, p, (uint32_t)num_sms(), kThreads, w4::kRing, 1u, dependent, s);
+    return launch(moe_up_kernel<kVec>, p, (uint32_t)num_sms(), kThreads, w4::kRing, 1u, true, s);
 }
 
 template <int kOut, bool kVec>
@@ -744,15 +756,14 @@ cudaError_t launch_moe_experts(const MoeExpertsArgs& a, bool routed, cudaStream_
     const Experts p{a.x, a.ldx, a.ids, a.weights, a.gq, a.gs, a.uq, a.us, a.dq, a.ds, a.g2, a.u2, a.d2,
                     work_of(a.work, (size_t)a.T, (size_t)a.k, (size_t)a.H, (size_t)a.I, &n), a.out, a.ldd,
                     (uint32_t)a.T, (uint32_t)a.k, (uint32_t)a.E, (uint32_t)a.H, (uint32_t)a.I};
-    if (!routed && a.dt == 0) {
-        moe_rows_kernel<<<(unsigned)a.T, 512, 0, s>>>(a.x, a.ldx, p.H, p.work);
+    if (!routed) {
+        if (a.dt == 0) moe_rows_kernel<0><<<(unsigned)a.T, 512, 0, s>>>(a.x, a.ldx, p.H, p.work);
+        else moe_rows_kernel<1><<<(unsigned)a.T, 512, 0, s>>>(a.x, a.ldx, p.H, p.work);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const bool dep = routed || a.dt == 0;                          // behind the router or moe_rows_kernel
     const bool vu = a.H % 64 == 0, vd = a.I % 64 == 0;             // (the scales are 16-byte aligned)
-    cudaError_t e = a.dt == 0 ? (vu ? run_up<0, true>(p, dep, s) : run_up<0, false>(p, dep, s))
-                              : (vu ? run_up<1, true>(p, dep, s) : run_up<1, false>(p, dep, s));
+    cudaError_t e = vu ? run_up<true>(p, s) : run_up<false>(p, s);  // behind the router or moe_rows_kernel
     if (e != cudaSuccess) return e;
     e = launch(moe_hidden_kernel, p, p.T * p.k, 256u, 0, 1u, true, s);
     if (e != cudaSuccess) return e;

@@ -231,21 +231,37 @@ __device__ __forceinline__ void mma_chunk(Acc<NT>& acc, const uint8_t* slot, con
     mma_step<kWide, NT>(acc, slot, [&](uint32_t j, uint32_t u) { return x0[j][u * m * 4u]; });
 }
 
-// Up to 8 token rows in global memory, row: this lane's (column g's), K elements of it, k0: where
-// the chunk begins.
+// Up to 8 token rows in global memory.  row: this lane's (column g's), chunk: where the step begins.
+// kWide: BF16 as the caller gave it, K elements.  Else FP16 in vector order, zero-padded to whole
+// chunks: the 32 vectors of a chunk as [u][t], so that the four lanes of a column read 64
+// consecutive bytes (in the natural order they touch four places 64 bytes apart, and L1 was what
+// bounded the gate / up product of 48 tokens: 85% busy, 176 us).
 template <bool kWide>
-__device__ __forceinline__ void mma_chunk_global(Acc<1>& acc, const uint8_t* slot, const uint16_t* row, uint32_t k0,
+__device__ __forceinline__ void mma_chunk_global(Acc<1>& acc, const uint8_t* slot, const uint16_t* row, uint32_t chunk,
                                                  uint32_t K)
 {
-    const uint32_t k = k0 + 32u * (threadIdx.x & 3u);
+    const uint32_t t = threadIdx.x & 3u;
     uint4 v[8];
 #pragma unroll
     for (uint32_t u = 0; u < 8; ++u) {
-        const uint32_t at = k + 128u * (u >> 2) + 8u * (u & 3u);
-        v[u] = at < K ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kWide) {
+            const uint32_t at = chunk * kChunk + 128u * (u >> 2) + 32u * t + 8u * (u & 3u);
+            v[u] = at < K ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            v[u] = *reinterpret_cast<const uint4*>(row + chunk * kChunk + 32u * u + 8u * t);
+        }
     }
     mma_step<kWide, 1>(acc, slot, [&](uint32_t, uint32_t u) { return v[u]; });
 }
+
+// Element offset, in a row in vector order, of the 8 values from 8 v on.
+__device__ __forceinline__ uint32_t vec_offset(uint32_t v)
+{
+    const uint32_t l = v & 31u;
+    return (v >> 5) * kChunk + (4u * (l >> 4) + (l & 3u)) * 32u + ((l & 15u) >> 2) * 8u;
+}
+
+__host__ __device__ inline uint32_t padded(uint32_t K) { return (K + kChunk - 1u) / kChunk * kChunk; }
 
 // ---------------------------------------------------------------- token rows into shared memory
 // Per token of a pass: exponent statistics and the factor that undoes its scaling.
