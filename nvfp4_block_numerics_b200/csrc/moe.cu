@@ -432,18 +432,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
         const uint32_t my_tiles = grp < S.ntile ? (S.ntile - grp + groups - 1u) / groups : 0u;
         const uint32_t steps = my_tiles * (wig < nch ? (nch - wig + wk - 1u) / wk : 0u);
         uint32_t lt = grp, lc = wig, ls = 0u;
-        size_t row = 0;                                            // byte offset of this lane's row pair
-        bool live = false, moved = true;
+        w4::Rows16 rw;
+        bool moved = true;
         auto load = [&](uint8_t* slot) {
             if (moved) {
                 while (ls + 1u < S.n && lt >= S.s[ls + 1u].tile0) ++ls;
                 const Seg& sg = S.s[ls];
                 const uint32_t i = (lt - sg.tile0) * sg.th + g;
-                live = g < sg.th && i < sg.n;
-                row = ((size_t)sg.expert * p.I + sg.i0 + i) * (p.H / 2u);
+                const bool live = g < sg.th && i < sg.n;
+                const size_t row = ((size_t)sg.expert * p.I + sg.i0 + i) * (p.H / 2u);
+                rw.set(p.gq + row, p.gs + row / 8u, p.uq + row, p.us + row / 8u, live, live);
                 moved = false;
             }
-            w4::load_chunk<kVec>(slot, p.gq + row, p.gs + row / 8u, p.uq + row, p.us + row / 8u, lc, p.H, live, live);
+            w4::load_chunk<kVec>(slot, rw, lc, p.H);
             lc += wk;
             if (lc >= nch) {
                 lc = wig;
@@ -589,16 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     const uint32_t steps = works ? (uint32_t)((uint64_t)(widx + 1u) * n / wpt) - s0 : 0u;
     uint32_t us = s0 / nch, uc = s0 - us * nch, ua = steps != 0u ? L.find(us) : 0u;
     uint32_t ls = us, lc = uc, la = ua;
-    size_t row = 0;
+    w4::Rows16 rw;
     bool moved = true;
     auto load = [&](uint8_t* slot) {
         if (moved) {
             if (ls >= L.sub[la + 1u]) ++la;
-            row = ((size_t)L.expert[la] * p.H + r0 + ta + g) * (p.I / 2u);
+            const size_t row = ((size_t)L.expert[la] * p.H + r0 + ta + g) * (p.I / 2u), row8 = row + (size_t)8u * (p.I / 2u);
+            rw.set(p.dq + row, p.ds + row / 8u, p.dq + row8, p.ds + row8 / 8u, g < tn, g + 8u < tn);
             moved = false;
         }
-        const size_t row8 = row + (size_t)8u * (p.I / 2u);
-        w4::load_chunk<kVec>(slot, p.dq + row, p.ds + row / 8u, p.dq + row8, p.ds + row8 / 8u, lc, p.I, g < tn, g + 8u < tn);
+        w4::load_chunk<kVec>(slot, rw, lc, p.I);
         if (++lc == nch) {
             lc = 0u;
             ++ls;

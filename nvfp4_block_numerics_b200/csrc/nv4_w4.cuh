@@ -40,52 +40,78 @@ constexpr int kDepth = 3;                         // chunks in flight per warp
 constexpr uint32_t kSlot = 16u * 128u + 16u * 16u;          // codes and scales of 16 rows x 256
 constexpr uint32_t kRing = kWarps * kDepth * kSlot;         // bytes for all warps
 
+// Copies n of kBytes (0 or kBytes) bytes and fills up with zeros.
 template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live)
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t n)
 {
-    // no byte is read and zeros are written where it is not live
     if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(live ? kBytes : 0)
-                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
 }
 
-// Starts the loads of chunk c of 16 weight rows into a ring slot: this lane's share of rows g and
-// g + 8 (qa, sa; qb, sb: where the rows' codes and scales begin; la, lb: whether they exist).
-// Slot: four 16-byte vectors per lane (row g halves 0 and 1, row g + 8 halves 0 and 1), then the
-// scales, 16 bytes per row.  kVec: K a multiple of 64 and 4-byte aligned scales; else 8 bytes of
-// codes at a time, scales byte by byte through registers.
+// Where this lane's share of a tile's rows g (a) and g + 8 (b) lies, and the bytes a copy of it
+// has (0: no such row).  Set once per tile; chunk c is a constant offset away.
+struct Rows16 {
+    const uint8_t *qa, *qb, *sa, *sb;
+    uint32_t na, nb;
+
+    __device__ __forceinline__ void set(const uint8_t* q0, const uint8_t* s0, const uint8_t* q1, const uint8_t* s1, bool la,
+                                        bool lb)
+    {
+        const uint32_t t = threadIdx.x & 3u;
+        qa = q0 + 16u * t;
+        qb = q1 + 16u * t;
+        sa = s0 + 4u * t;
+        sb = s1 + 4u * t;
+        na = la ? 16u : 0u;
+        nb = lb ? 16u : 0u;
+    }
+};
+
+// Starts the loads of chunk c of 16 weight rows into a ring slot.  Slot: four 16-byte vectors per
+// lane (row g halves 0 and 1, row g + 8 halves 0 and 1), then the scales, 16 bytes per row.
+// kVec: K a multiple of 64 and 4-byte aligned scales; else 8 bytes of codes at a time, scales byte
+// by byte through registers.
 template <bool kVec>
-__device__ __forceinline__ void load_chunk(uint8_t* slot, const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
-                                           const uint8_t* sb, uint32_t c, uint32_t K, bool la, bool lb)
+__device__ __forceinline__ void load_chunk(uint8_t* slot, const Rows16& r, uint32_t c, uint32_t K)
 {
     const uint32_t lane = threadIdx.x & 31u, t = lane & 3u;
-    const uint32_t dst = smem_u32(slot) + 16u * lane, ks = c * kChunk + 64u * t;
+    const uint32_t dst = smem_u32(slot) + 16u * lane, sdst = smem_u32(slot) + 2048u + 4u * lane;   // scales: row g, word t
+    const uint8_t *qa = r.qa + c * 128u, *qb = r.qb + c * 128u, *sa = r.sa + c * 16u, *sb = r.sb + c * 16u;
+    if (kVec && (c + 1u) * kChunk <= K) {
+        cp_async<16>(dst, qa, r.na);
+        cp_async<16>(dst + 512u, qa + 64u, r.na);
+        cp_async<16>(dst + 1024u, qb, r.nb);
+        cp_async<16>(dst + 1536u, qb + 64u, r.nb);
+        cp_async<4>(sdst, sa, r.na >> 2);
+        cp_async<4>(sdst + 128u, sb, r.nb >> 2);
+        return;
+    }
+    const uint32_t ks = c * kChunk + 64u * t;
 #pragma unroll
     for (uint32_t p = 0; p < 2; ++p) {
         const uint32_t k = c * kChunk + 128u * p + 32u * t;
         if constexpr (kVec) {
-            cp_async<16>(dst + 512u * p, qa + k / 2u, la && k < K);
-            cp_async<16>(dst + 1024u + 512u * p, qb + k / 2u, lb && k < K);
+            cp_async<16>(dst + 512u * p, qa + 64u * p, k < K ? r.na : 0u);
+            cp_async<16>(dst + 1024u + 512u * p, qb + 64u * p, k < K ? r.nb : 0u);
         } else {
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
-                cp_async<8>(dst + 512u * p + 8u * j, qa + k / 2u + 8u * j, la && k + 16u * j < K);
-                cp_async<8>(dst + 1024u + 512u * p + 8u * j, qb + k / 2u + 8u * j, lb && k + 16u * j < K);
+                cp_async<8>(dst + 512u * p + 8u * j, qa + 64u * p + 8u * j, k + 16u * j < K ? r.na >> 1 : 0u);
+                cp_async<8>(dst + 1024u + 512u * p + 8u * j, qb + 64u * p + 8u * j, k + 16u * j < K ? r.nb >> 1 : 0u);
             }
         }
     }
-    const uint32_t sdst = smem_u32(slot) + 2048u + 4u * lane;      // row g = lane / 4, word t
     if constexpr (kVec) {
-        cp_async<4>(sdst, sa + ks / 16u, la && ks < K);
-        cp_async<4>(sdst + 128u, sb + ks / 16u, lb && ks < K);
+        cp_async<4>(sdst, sa, ks < K ? r.na >> 2 : 0u);
+        cp_async<4>(sdst + 128u, sb, ks < K ? r.nb >> 2 : 0u);
     } else {
         uint32_t a = 0u, b = 0u;
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
-            if (la && ks + 16u * j < K) a |= (uint32_t)__ldg(sa + ks / 16u + j) << (8u * j);
-            if (lb && ks + 16u * j < K) b |= (uint32_t)__ldg(sb + ks / 16u + j) << (8u * j);
+            if (r.na != 0u && ks + 16u * j < K) a |= (uint32_t)__ldg(sa + j) << (8u * j);
+            if (r.nb != 0u && ks + 16u * j < K) b |= (uint32_t)__ldg(sb + j) << (8u * j);
         }
         *reinterpret_cast<uint32_t*>(slot + 2048u + 4u * lane) = a;
         *reinterpret_cast<uint32_t*>(slot + 2048u + 128u + 4u * lane) = b;

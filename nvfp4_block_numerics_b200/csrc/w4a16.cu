@@ -56,18 +56,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     for (uint32_t p0 = 0; p0 < p.T; p0 += p.cap) {
         const uint32_t m = min(p.cap, p.T - p0);
         uint32_t lt = grp, lc = wig;              // the step to load next
-        size_t row = 0;                           // byte offset of row g's codes of the tile to load
-        bool la = false, lb = false, moved = true;
+        Rows16 rw;
+        bool moved = true;
         auto load = [&](uint8_t* slot) {
             if (moved) {
                 const uint32_t a = r0 + lt * p.tile, n = min(p.tile, r0 + R - min(a, r0 + R));
-                row = (size_t)(a + g) * (p.K / 2u);
-                la = g < n;
-                lb = g + 8u < n;
+                const size_t row = (size_t)(a + g) * (p.K / 2u), row8 = row + (size_t)8u * (p.K / 2u);
+                rw.set(p.q + row, p.sc + row / 8u, p.q + row8, p.sc + row8 / 8u, g < n, g + 8u < n);
                 moved = false;
             }
-            const size_t row8 = row + (size_t)8u * (p.K / 2u);
-            load_chunk<kVec>(slot, p.q + row, p.sc + row / 8u, p.q + row8, p.sc + row8 / 8u, ch0 + lc, p.K, la, lb);
+            load_chunk<kVec>(slot, rw, ch0 + lc, p.K);
             lc += wk;
             if (lc >= nch) {
                 lc = wig;
