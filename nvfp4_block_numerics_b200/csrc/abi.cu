@@ -556,7 +556,6 @@ nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, i
                             const uint8_t* scales, const float* d_s2, int64_t N, nv4_dtype out_dt, void* out,
                             int64_t ldd, uint32_t* d_flags, void* stream)
 {
-    (void)d_flags;
     if (dt != NV4_BF16 && dt != NV4_FP16) return NV4_ERR_DTYPE;
     if (out_dt != NV4_BF16 && out_dt != NV4_FP16 && out_dt != NV4_FP32) return NV4_ERR_DTYPE;
     if (T < 0 || N < 0 || K < 0 || K % 16 != 0 || ldx < K || ldd < N) return NV4_ERR_SHAPE;
@@ -564,7 +563,11 @@ nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, i
     if (K == 0) return NV4_ERR_SHAPE;
     if (x == nullptr || q == nullptr || scales == nullptr || d_s2 == nullptr || out == nullptr) return NV4_ERR_NULL;
     if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned16(out) || ldx % 8 != 0) return NV4_ERR_ALIGN;
-    if (K > kMaxW4K || T >= (int64_t)1 << 31 || N >= (int64_t)1 << 31) return NV4_ERR_LIMIT;
+    if (K > kMaxW4K || T >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || ((T + 31) / 32) * ((N + 127) / 128) >= (int64_t)1 << 31)
+        return NV4_ERR_LIMIT;
+    if (T > 16)
+        return from_cuda(launch_linear_w4a16_mma(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd, d_flags,
+                                                 (cudaStream_t)stream));
     return from_cuda(launch_linear_w4a16(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd,
                                          (cudaStream_t)stream));
 }

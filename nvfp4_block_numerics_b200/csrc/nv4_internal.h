@@ -92,6 +92,9 @@ constexpr size_t kMaxSmemW4 = 220u * 1024u;
 cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
                                 cudaStream_t s);
+cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
+                                    const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
+                                    uint32_t* d_flags, cudaStream_t s);
 // Mixture-of-experts limits: tokens and (token, expert) pairs of a call, experts, experts per
 // token, widths.
 constexpr int64_t kMaxMoeTokens = 64, kMaxMoePairs = 2048, kMaxMoeExperts = 512, kMaxMoeTopK = 32;

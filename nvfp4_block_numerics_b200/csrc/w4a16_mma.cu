@@ -1,0 +1,506 @@
+// w4a16_mma.cu -- the weight-only linear layer for many rows, on the 5th-generation tensor cores
+// (sm_100a): BF16 / FP16 rows times NVFP4 weights.
+//
+// [CAL] layer table (W4A16); the few-row form is in w4a16.cu.  out^T tile = W tile * x tile^T: the
+// 128 weight rows of a tile are the MMA's M, kTok rows of x its N.  The MMA takes no FP4 beside
+// 16-bit operands, so the codes are decoded on the way: e2m1 * e4m3 is exact in BF16 and FP16.
+// The decoded operand goes to TENSOR memory, not to shared memory: tcgen05.mma reads its A operand
+// from there, so a decoded byte is written once and read without shared memory, which the x tiles
+// already keep busy (a 128 x 256 x 64 step moves 32 KB of x in and 32 KB out of it in 512 clocks).
+//
+// Persistent, one CTA per SM, 20 warps:
+//   * warp 0, one lane: 2-D TMA of x, kTok rows x 64 K-elements per stage (128-byte swizzle, zeros
+//     outside), a ring of kStages that runs across tiles.
+//   * warp 1: owns the tensor memory; one lane issues four MMAs (K = 16) per stage.
+//   * warps 4-11: decoders, thread = weight row (the tensor memory lane it may write), two sets of
+//     four warps that take alternate stages.  A thread loads its row's 32 bytes of codes and 4
+//     scales of the stage after next while it decodes, and writes 32 columns (tcgen05.st).
+//   * warps 12-19: epilogue, two warps per 32 lanes, half the columns each; 16-bit outputs leave
+//     through a 2 KB transpose per warp so that a store covers 64 bytes of an output row.
+// With few tiles a cluster of z CTAs shares one: each multiplies its part of K, the partial sums
+// meet through distributed shared memory and are added in rank order.
+// Every mbarrier wait is bounded (kWaitLimitNs), as in gemm.cu.
+#include <type_traits>
+
+#include "nv4_internal.h"
+#include "nv4_tcgen05.cuh"
+#include "nv4_tensormap.h"
+
+namespace nv4 {
+
+namespace w4mma {
+
+using namespace tc;
+
+constexpr int kThreads = 640;
+constexpr int kABufs = 4;                         // decoded stages in tensor memory, 32 columns each
+constexpr uint32_t kACol = 256;                   // behind the accumulator's columns
+constexpr int kStages = 6;
+
+struct Params {
+    CUtensorMap map_x;                            // x [T, K], boxes of kTok rows x 64 elements
+    const uint8_t* q;
+    const uint8_t* sc;
+    const float* d_s2;
+    void* out;
+    int64_t ldd;
+    uint32_t T, N, K, z, n_tiles, tiles, stages;  // n_tiles: of 128 weight rows; stages of 64 K-elements
+    uint32_t vec;                                 // 16-byte stores of 16-bit outputs are aligned
+    uint32_t* d_flags;
+};
+
+template <int kTok>
+struct Smem {
+    uint8_t x[kStages][kTok * 128];               // 1024-byte aligned
+    uint8_t stg[8][2048];
+    uint64_t full[kStages], empty[kStages], a_full[kABufs], a_free[kABufs], acc_full, acc_empty, drain;
+    uint32_t tmem_base, abort, issued, consumed;
+};
+
+// One K = 16 step, A in tensor memory.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 64 codes and 4 scales of a weight row from element k on; zeros past K or where not live.
+template <bool kVec>
+__device__ __forceinline__ void load64(uint32_t (&q)[8], uint32_t& s, const uint8_t* qrow, const uint8_t* srow, uint32_t k,
+                                       uint32_t K, bool live)
+{
+    s = 0u;
+    if constexpr (kVec) {
+        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+        if (live && k < K) {
+            a = __ldg(reinterpret_cast<const uint4*>(qrow + (k >> 1)));
+            b = __ldg(reinterpret_cast<const uint4*>(qrow + (k >> 1) + 16u));
+            s = __ldg(reinterpret_cast<const uint32_t*>(srow + (k >> 4)));
+        }
+        q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
+        q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            uint2 v = make_uint2(0u, 0u);
+            if (live && k + 16u * j < K) {
+                v = __ldg(reinterpret_cast<const uint2*>(qrow + (k >> 1) + 8u * j));
+                s |= (uint32_t)__ldg(srow + (k >> 4) + j) << (8u * j);
+            }
+            q[2 * j] = v.x;
+            q[2 * j + 1] = v.y;
+        }
+    }
+}
+
+// The 64 values as 32 words of two: FP16 by conversion and multiply, BF16 by converting those
+// (at most 6 significant bits: exact both times).
+template <int kDt>
+__device__ __forceinline__ void decode64(uint32_t (&o)[32], const uint32_t (&q)[8], uint32_t s)
+{
+    uint32_t p[4];
+    {
+        uint32_t a, b;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(s & 0xFFFFu)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(s >> 16)));
+        p[0] = __byte_perm(a, a, 0x1010);
+        p[1] = __byte_perm(a, a, 0x3232);
+        p[2] = __byte_perm(b, b, 0x1010);
+        p[3] = __byte_perm(b, b, 0x3232);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        uint32_t h[4];
+        cvt_e2m1x8_to_f16x8(q[u], h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t r;
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h[i]), "r"(p[u >> 1]));
+            if constexpr (kDt == 0) {
+                float lo, hi;
+                f16x2_to_f32(r, lo, hi);
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+            }
+            o[4 * u + i] = r;
+        }
+    }
+}
+
+template <int kOut>
+__device__ __forceinline__ uint16_t to16(float v)
+{
+    uint16_t b;
+    if constexpr (kOut == 0)
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v));
+    else
+        asm("cvt.rn.f16.f32 %0, %1;" : "=h"(b) : "f"(v));
+    return b;
+}
+
+template <int kOut>
+__device__ __forceinline__ void store1(void* out, int64_t at, float v)
+{
+    if constexpr (kOut == 2) static_cast<float*>(out)[at] = v;
+    else static_cast<uint16_t*>(out)[at] = to16<kOut>(v);
+}
+
+template <int kTok, int kDt, int kOut, bool kVec>
+__global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_constant__ Params p)
+{
+    // kind::f16: FP32 accumulator (bit 4), A and B types in bits 7 and 10 (0 FP16, 1 BF16), both
+    // K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28
+    constexpr uint32_t kIdesc = (1u << 4) | (kDt == 0 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTok >> 3) << 17) |
+                                ((128u >> 4) << 24);
+    extern __shared__ uint8_t smem_raw[];
+    Smem<kTok>& sm = *reinterpret_cast<Smem<kTok>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<kTok>) + 15u) & ~size_t(15)));   // [kTok][128], z > 1
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.z > 1u ? cluster_ctarank() : 0u;
+    const uint32_t clu = blockIdx.x / p.z, nclu = gridDim.x / p.z;
+    const uint32_t ks0 = rank * p.stages / p.z, KS = (rank + 1u) * p.stages / p.z - ks0;   // this CTA's stages of a tile
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < kABufs; ++b) {
+            mbar_init(&sm.a_full[b], 4);                           // the four warps of a decoder set
+            mbar_init(&sm.a_free[b], 1);
+        }
+        mbar_init(&sm.acc_full, 1);
+        mbar_init(&sm.acc_empty, 8);
+        mbar_init(&sm.drain, 1);
+        sm.abort = sm.issued = sm.consumed = 0u;
+        mbar_init_fence();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map_x)) : "memory");
+    }
+    if (warp == 1) tmem_alloc(&sm.tmem_base, 512u);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    uint32_t flags = 0u;
+    auto aborted = [&]() { return *reinterpret_cast<volatile uint32_t*>(&sm.abort) != 0u; };
+    auto give_up = [&]() { flags |= kFlagTimeout; atomicOr(&sm.abort, 1u); };
+
+    if (warp == 0) {
+        if (lane == 0) {                                           // producer of x
+            uint32_t g = 0;
+            for (uint32_t t = clu; t < p.tiles && !aborted(); t += nclu) {
+                const int tok0 = (int)((t / p.n_tiles) * kTok);
+                for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
+                    const uint32_t s = g % kStages;
+                    if (g >= (uint32_t)kStages && !mbar_wait(&sm.empty[s], ((g / kStages) - 1u) & 1u)) give_up();
+                    if (aborted()) break;
+                    mbar_arrive_expect_tx(&sm.full[s], kTok * 128u);
+                    tma_load_2d(sm.x[s], &p.map_x, &sm.full[s], (int)((ks0 + ks) * 64u), tok0);
+                }
+            }
+            sm.issued = g;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {                                           // MMA issuer
+            uint32_t g = 0, i = 0;
+            for (uint32_t t = clu; t < p.tiles && !aborted(); t += nclu, ++i) {
+                if (i > 0 && !mbar_wait(&sm.acc_empty, (i - 1u) & 1u)) {
+                    give_up();
+                    break;
+                }
+                tc_fence_after();
+                for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
+                    const uint32_t s = g % kStages, b = g % kABufs;
+                    if (!mbar_wait(&sm.full[s], (g / kStages) & 1u) || !mbar_wait(&sm.a_full[b], (g / kABufs) & 1u)) {
+                        give_up();
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t x0 = smem_u32(sm.x[s]), a0 = tmem + kACol + 32u * b;
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        mma_f16(tmem, a0 + 8u * j, smem_desc(x0 + 32u * j, 1u, 64u, 2u), kIdesc, (ks | j) != 0u ? 1u : 0u);
+                    tc_commit(&sm.empty[s]);
+                    tc_commit(&sm.a_free[b]);
+                }
+                if (aborted()) break;
+                tc_commit(&sm.acc_full);
+            }
+            sm.consumed = g;
+            tc_commit(&sm.drain);
+            if (!mbar_wait(&sm.drain, 0u)) flags |= kFlagTimeout;
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        // ---- decoders: set 0 the even, set 1 the odd stages (counted over all tiles)
+        const uint32_t quad = (uint32_t)warp & 3u, lanes = (32u * quad) << 16;
+        uint32_t t = clu, ks = 0u, g = ((uint32_t)warp - 4u) >> 2;
+        const uint8_t *qrow = nullptr, *srow = nullptr;
+        bool live = false;
+        auto settle = [&]() {                                      // (t, ks) of stage ks past the tile's end
+            while (t < p.tiles && ks >= KS) {
+                ks -= KS;
+                t += nclu;
+            }
+        };
+        auto fetch = [&](uint32_t (&q)[8], uint32_t& s) {
+            if (t >= p.tiles) return;
+            const uint32_t row = (t % p.n_tiles) * 128u + 32u * quad + (uint32_t)lane;
+            live = row < p.N;
+            qrow = p.q + (size_t)row * (p.K / 2u);
+            srow = p.sc + (size_t)row * (p.K / 16u);
+            load64<kVec>(q, s, qrow, srow, (ks0 + ks) * 64u, p.K, live);
+        };
+        ks = g;
+        settle();
+        uint32_t q[8], s = 0u;
+        fetch(q, s);
+        bool quit = false;
+        while (t < p.tiles && !quit) {
+            uint32_t o[32];
+            decode64<kDt>(o, q, s);
+            ks += 2u;
+            settle();
+            fetch(q, s);                                           // the set's next stage, in flight from here
+            const uint32_t b = g % kABufs;
+            const bool ok = g < (uint32_t)kABufs || mbar_wait(&sm.a_free[b], ((g / kABufs) - 1u) & 1u);
+            const bool timed_out = __any_sync(0xFFFFFFFFu, !ok);
+            quit = timed_out || __any_sync(0xFFFFFFFFu, aborted());
+            if (quit) {
+                if (timed_out && lane == 0) give_up();
+                break;
+            }
+            tc_fence_after();
+            tmem_st<32>(tmem + lanes + kACol + 32u * b, o);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.a_full[b]);
+            g += 2u;
+        }
+        __syncwarp();
+    } else if (warp >= 12) {
+        // ---- epilogue: lanes 32 quad .. + 31 (one weight row per thread), columns (tokens) of half h
+        const uint32_t quad = (uint32_t)warp & 3u, h = warp >= 16 ? 1u : 0u;
+        uint8_t* st = sm.stg[warp - 12];
+        const float s2 = *p.d_s2;
+        constexpr uint32_t kCols = kTok / 2;
+        uint32_t i = 0;
+        for (uint32_t t = clu; t < p.tiles; t += nclu, ++i) {
+            const bool ok = !aborted() && mbar_wait(&sm.acc_full, i & 1u);
+            if (!ok) {
+                if (!aborted()) give_up();
+                break;
+            }
+            tc_fence_after();
+            __syncwarp();
+            const uint32_t n0 = (t % p.n_tiles) * 128u + 32u * quad, tok0 = (t / p.n_tiles) * kTok + h * kCols;
+            const uint32_t taddr = tmem + ((32u * quad) << 16) + h * kCols;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.acc_empty);
+            };
+            if (p.z > 1u) {                                        // (one tile per cluster)
+#pragma unroll 1
+                for (uint32_t c = 0; c < kCols; c += 16u) {
+                    float v[16];
+                    tmem_ld16(taddr + c, v);
+#pragma unroll
+                    for (uint32_t k = 0; k < 16; ++k) part[(h * kCols + c + k) * 128u + 32u * quad + lane] = v[k];
+                }
+                release();
+                continue;
+            }
+            if constexpr (kOut == 2) {
+#pragma unroll 1
+                for (uint32_t c = 0; c < kCols; c += 16u) {
+                    float v[16];
+                    tmem_ld16(taddr + c, v);
+#pragma unroll
+                    for (uint32_t k = 0; k < 16; ++k)
+                        if (tok0 + c + k < p.T && n0 + lane < p.N)
+                            static_cast<float*>(p.out)[(int64_t)(tok0 + c + k) * p.ldd + n0 + lane] = v[k] * s2;
+                }
+                release();
+            } else {
+                // converted into registers first: the accumulator is released before the stores
+                uint32_t w[kCols / 2];
+#pragma unroll
+                for (uint32_t c = 0; c < kCols; c += 16u) {
+                    float v[16];
+                    tmem_ld16(taddr + c, v);
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k)
+                        w[c / 2 + k] = (uint32_t)to16<kOut>(v[2 * k] * s2) | (uint32_t)to16<kOut>(v[2 * k + 1] * s2) << 16;
+                }
+                release();
+                const bool vec = p.vec != 0u && n0 + 32u <= p.N;
+#pragma unroll
+                for (uint32_t c = 0; c < kCols; c += 32u) {
+                    constexpr uint32_t kBlk = kCols < 32u ? kCols : 32u;   // tokens per block
+#pragma unroll
+                    for (uint32_t k = 0; k < kBlk; ++k)            // [token][32 rows] of 16 bits
+                        *reinterpret_cast<uint16_t*>(st + 64u * k + 2u * lane) = (uint16_t)(w[(c + k) / 2] >> (16u * (k & 1u)));
+                    __syncwarp();
+                    if (vec) {
+#pragma unroll
+                        for (uint32_t k = 0; k < kBlk / 8u; ++k) {
+                            const uint32_t tok = 8u * k + ((uint32_t)lane >> 2), at = tok0 + c + tok;
+                            const uint4 x = *reinterpret_cast<const uint4*>(st + 64u * tok + 16u * (lane & 3));
+                            if (at < p.T)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (int64_t)at * p.ldd + n0 + 8u * (lane & 3)) = x;
+                        }
+                    } else {
+                        for (uint32_t k = 0; k < kBlk; ++k)
+                            if (tok0 + c + k < p.T && n0 + lane < p.N)
+                                static_cast<uint16_t*>(p.out)[(int64_t)(tok0 + c + k) * p.ldd + n0 + lane] =
+                                    *reinterpret_cast<const uint16_t*>(st + 64u * k + 2u * lane);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+
+    // ---- teardown: copies loaded but never multiplied, the cluster's sums, tensor memory
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (uint32_t g = sm.consumed; g < sm.issued; ++g)
+            if (!mbar_wait(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
+    if (p.z > 1u) {
+        cluster_sync();
+        const uint32_t n0 = (clu % p.n_tiles) * 128u, tok0 = (clu / p.n_tiles) * kTok;
+        const float s2 = *p.d_s2;
+        const uint32_t rows = min(128u, p.N - n0), toks = min((uint32_t)kTok, p.T - tok0);
+        const uint32_t j1 = (rank + 1u) * toks / p.z;
+        for (uint32_t i = (rank * toks / p.z) * 128u + threadIdx.x; i < j1 * 128u; i += kThreads) {
+            const uint32_t r = i & 127u, tok = i >> 7;
+            if (r >= rows) continue;
+            float v[8], sum = 0.0f;
+#pragma unroll
+            for (uint32_t k = 0; k < 8u; ++k) v[k] = k < p.z ? ld_dsmem_f32(part + i, k) : 0.0f;
+#pragma unroll
+            for (uint32_t k = 0; k < 8u; ++k) sum += v[k];
+            if (!aborted()) store1<kOut>(p.out, (int64_t)(tok0 + tok) * p.ldd + n0 + r, sum * s2);
+        }
+        cluster_sync();                                            // the others have read this CTA's sums
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512u);
+    }
+    flags = __reduce_or_sync(0xFFFFFFFFu, flags);
+    if (lane == 0) flag_or(p.d_flags, flags);
+}
+
+static bool x_map(CUtensorMap* map, const void* x, int dt, int64_t T, int64_t K, int64_t ldx, uint32_t box_rows)
+{
+    auto enc = encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T};
+    const cuuint64_t strides[1] = {(cuuint64_t)ldx * 2u};
+    const cuuint32_t box[2] = {64u, box_rows};
+    const cuuint32_t es[2] = {1u, 1u};
+    return enc(map, dt == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(x),
+               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kTok, int kDt, int kOut, bool kVec>
+static cudaError_t run(const Params& p, cudaStream_t s)
+{
+    static bool ready[64] = {};
+    auto kern = linear_mma_kernel<kTok, kDt, kOut, kVec>;
+    const size_t base = sizeof(Smem<kTok>) + 1024 + 16, part = kTok <= 128 ? (size_t)kTok * 512u : 0u;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(base + part));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    const uint32_t sms = (uint32_t)num_sms();
+    cfg.gridDim = dim3(p.z > 1u ? p.tiles * p.z : p.tiles < sms ? p.tiles : sms, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = base + (p.z > 1u ? part : 0u);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.z;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.z > 1u ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int kTok>
+static cudaError_t pick(const Params& p, int dt, int out_dt, bool vec, cudaStream_t s)
+{
+    auto by_out = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (out_dt == 0) return vec ? run<kTok, D, 0, true>(p, s) : run<kTok, D, 0, false>(p, s);
+        if (out_dt == 1) return vec ? run<kTok, D, 1, true>(p, s) : run<kTok, D, 1, false>(p, s);
+        return vec ? run<kTok, D, 2, true>(p, s) : run<kTok, D, 2, false>(p, s);
+    };
+    return dt == 0 ? by_out(std::integral_constant<int, 0>{}) : by_out(std::integral_constant<int, 1>{});
+}
+
+}  // namespace w4mma
+
+cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
+                                    const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
+                                    uint32_t* d_flags, cudaStream_t s)
+{
+    using namespace w4mma;
+    Params p = {};
+    p.q = q;
+    p.sc = sc;
+    p.d_s2 = d_s2;
+    p.out = out;
+    p.ldd = ldd;
+    p.T = (uint32_t)T;
+    p.N = (uint32_t)N;
+    p.K = (uint32_t)K;
+    p.n_tiles = (uint32_t)((N + 127) / 128);
+    p.stages = (uint32_t)((K + 63) / 64);
+    p.vec = ldd % 8 == 0 ? 1u : 0u;
+    p.d_flags = d_flags;
+    const uint32_t sms = (uint32_t)num_sms();
+    // the widest token tile that the rows fill; half of it where that leaves SMs without a tile
+    uint32_t tok = T <= 32 ? 32u : T <= 64 ? 64u : T <= 128 ? 128u : 256u;
+    auto tiles = [&](uint32_t k) { return p.n_tiles * (uint32_t)((T + k - 1) / k); };
+    if (tok == 256u && tiles(256u) < sms) tok = 128u;
+    p.tiles = tiles(tok);
+    // split K in clusters while there are SMs for it and every CTA keeps four stages
+    p.z = 1u;
+    while (tok <= 128u && p.z < 8u && p.tiles * p.z * 2u <= sms && p.stages >= 8u * p.z) p.z *= 2u;
+    if (!x_map(&p.map_x, x, dt, T, K, ldx, tok)) return cudaErrorInvalidValue;
+    const bool vec = K % 64 == 0;                                  // (32-byte code runs, 4-byte aligned scales)
+    if (tok == 32u) return pick<32>(p, dt, out_dt, vec, s);
+    if (tok == 64u) return pick<64>(p, dt, out_dt, vec, s);
+    if (tok == 128u) return pick<128>(p, dt, out_dt, vec, s);
+    return pick<256>(p, dt, out_dt, vec, s);
+}
+
+}  // namespace nv4

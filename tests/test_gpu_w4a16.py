@@ -68,6 +68,17 @@ def test_linear_odd_sizes(orc, N, K, T):
     check(orc, rows(rng, T, K, "bf16").to(G.DEV), q, sc, 1.0, "fp32")
 
 
+@pytest.mark.parametrize("T,N,K,dt,out", [
+    (33, 3000, 4096, "bf16", "bf16"), (128, 128, 64, "fp16", "fp32"), (129, 140, 192, "bf16", "fp16"),
+    (256, 256, 2048, "bf16", "bf16"), (600, 2880, 656, "fp16", "bf16"), (1025, 5000, 320, "bf16", "fp32"),
+    (700, 20000, 80, "bf16", "bf16")])
+def test_linear_many_rows(orc, T, N, K, dt, out):
+    """Every token tile width, clusters that split K and tiles that wrap around the SMs."""
+    rng = np.random.default_rng(T * N)
+    q, sc = weights(rng, N, K)
+    check(orc, rows(rng, T, K, dt).to(G.DEV), q, sc, 0.0031, out)
+
+
 @pytest.mark.parametrize("T", [1, 9, 70])
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_linear_strides(orc, T, dt):
