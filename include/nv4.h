@@ -479,6 +479,16 @@ NV4_API nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, con
                           const uint8_t* sfb_mma, int64_t M, int64_t N, int64_t K, nv4_dtype out_dt,
                           void* out, int64_t ldd, uint32_t* d_flags, void* stream);
 
+/* nv4_linear_mxfp4 -- the W4A4 linear layer: nv4_mxfp4_quant_mma of x [M, K] (dt NV4_BF16 or
+ * NV4_FP32), then nv4_gemm_mxfp4 with the weights qw, sfw_mma [N, K].  The rules of both apply.
+ * d_work: nv4_linear_mxfp4_work_bytes(M, K) bytes, 16-byte aligned, not shared by calls that may
+ * run at the same time; nothing has to be in it and nothing is kept in it (NV4_ERR_LIMIT if
+ * work_bytes is less). */
+NV4_API size_t nv4_linear_mxfp4_work_bytes(int64_t M, int64_t K);
+NV4_API nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, int64_t ldx,
+                            const uint8_t* qw, const uint8_t* sfw_mma, int64_t N, nv4_dtype out_dt, void* out,
+                            int64_t ldd, void* d_work, size_t work_bytes, uint32_t* d_flags, void* stream);
+
 /* ---------------------------------------------------------------------------
  * nv4_linear_w4a16 -- the weight-only linear layer on NVFP4 weights ([CAL] layer table:
  * W4A16 layers, activations kept in 16 bits).

@@ -31,7 +31,7 @@ __all__ = [
     "nv4_tensor_amax_batched", "nv4_act_quant_batched", "nv4_dequant_batched", "nv4_weight_quant_rtn_batched",
     "nv4_linear_w4a16", "linear_w4a16", "nv4_moe_route", "nv4_moe_work_bytes", "nv4_moe_experts", "nv4_moe_layer",
     "moe_route", "moe_experts", "moe_layer", "ExpertWeights", "nv4_mxfp4_mma_scale_bytes", "nv4_mxfp4_quant_mma",
-    "nv4_gemm_mxfp4", "mxfp4_quant_mma", "gemm_mxfp4", "linear_mxfp4",
+    "nv4_gemm_mxfp4", "nv4_linear_mxfp4", "nv4_linear_mxfp4_work_bytes", "mxfp4_quant_mma", "gemm_mxfp4", "linear_mxfp4",
 ]
 
 BF16, FP16, FP32 = 0, 1, 2
@@ -106,6 +106,9 @@ _SIGS = {
     "nv4_mxfp4_mma_scale_bytes": (C.c_size_t, [_i64, _i64]),
     "nv4_mxfp4_quant_mma": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "nv4_gemm_mxfp4": (C.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _i64, _vp, _vp]),
+    "nv4_linear_mxfp4_work_bytes": (C.c_size_t, [_i64, _i64]),
+    "nv4_linear_mxfp4": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _i64, C.c_int, _vp, _i64, _vp, C.c_size_t, _vp,
+                                   _vp]),
     "nv4_moe_route": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _i64, C.c_int, C.c_int, _vp, _vp, _vp, _vp]),
     "nv4_moe_work_bytes": (C.c_size_t, [_i64, C.c_int, _i64, _i64]),
     "nv4_moe_experts": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, C.c_int, _i64, _i64,
@@ -132,6 +135,8 @@ _SIGS = {
 def lib() -> C.CDLL:
     """Load libnv4.so (built in-tree by nvfp4_block_numerics_b200.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -715,25 +720,40 @@ def mxfp4_to_nvfp4(mx_q, e8m0, in_place=False, d_counts=None, d_flags=None, stre
 
 
 # ------------------------------------------------------------------ products on FP4 weights
-def _here(x: torch.Tensor, *others):
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _here(x: torch.Tensor, *others) -> int:
     """All tensors of a product live on the current device: the library launches there."""
-    if not x.is_cuda:
+    d = x.get_device()
+    if d < 0:
         raise NV4Error("tensor must live on a CUDA device")
-    d = x.device
-    if d.index != torch.cuda.current_device():
-        raise NV4Error(f"tensors live on {d}: make it the current device (torch.cuda.device)")
+    if d != _current_device():
+        raise NV4Error(f"tensors live on cuda:{d}: make it the current device (torch.cuda.device)")
     for t in others:
-        if t is not None and t.device != d:
-            raise NV4Error(f"tensors live on different devices ({d}, {t.device})")
+        if t is not None and t.get_device() != d:
+            raise NV4Error(f"tensors live on different devices (cuda:{d}, {t.device})")
+    return d
+
+
+def _on(stream, d: int) -> int:
+    return _raw_stream(d) if stream is None else _stream(stream)
 
 
 def _new(shape, dtype, x: torch.Tensor, stream) -> torch.Tensor:
     """An output allocated for the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=x.device)
+        return x.new_empty(shape, dtype=dtype)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=x.device)
     with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=x.device)
+        return x.new_empty(shape, dtype=dtype)
+
+
+def _bytes(t: torch.Tensor, shape, name: str) -> int:
+    if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+        raise NV4Error(f"{name} must be a contiguous uint8 tensor {tuple(shape)}")
+    return t.data_ptr()
 
 
 def _f32_n(t: torch.Tensor, n: int, name: str):
@@ -752,21 +772,18 @@ def _rows16(x: torch.Tensor, name: str):
 def nv4_linear_w4a16(x, q, scales, d_s2, out, d_flags=None, stream=None):
     """out[t, n] = s2 * sum_k x[t, k] * W[n, k]: bf16 / float16 rows x [T, K], NVFP4 weights
     (codes [N, K/2], E4M3 scales [N, K/16], s2)."""
-    _here(x, q, scales, d_s2, out, d_flags)
+    dev = _here(x, q, scales, d_s2, out, d_flags)
     T, K, ldx = _rows16(x, "x")
-    if q.dim() != 2:
-        raise NV4Error("q must be [N, K/2]")
     N = q.shape[0]
-    _u8(q, (N, K // 2), "q")
-    _u8(scales, (N, K // 16), "scales")
     if out.dtype not in _DT:
         raise NV4Error("out must be bf16, float16 or float32")
     orows, ocols, ldd = _rowmajor(out, "out")
-    if (orows, ocols) != (T, N):
+    if orows != T or ocols != N:
         raise NV4Error("out must be [T, N]")
-    _check(lib().nv4_linear_w4a16(x.data_ptr(), _DT[x.dtype], T, K, ldx, q.data_ptr(), scales.data_ptr(),
-                                  _f32_n(d_s2, 1, "d_s2"), N, _DT[out.dtype], out.data_ptr(),
-                                  max(ldd, N) if T <= 1 else ldd, _ptr(d_flags), _stream(stream)), "nv4_linear_w4a16")
+    _check(lib().nv4_linear_w4a16(x.data_ptr(), _DT[x.dtype], T, K, ldx, _bytes(q, (N, K // 2), "q"),
+                                  _bytes(scales, (N, K // 16), "scales"), _f32_n(d_s2, 1, "d_s2"), N, _DT[out.dtype],
+                                  out.data_ptr(), max(ldd, N) if T <= 1 else ldd, _ptr(d_flags), _on(stream, dev)),
+           "nv4_linear_w4a16")
 
 
 def linear_w4a16(x, q, scales, d_s2, dtype=None, d_flags=None, stream=None):
@@ -779,9 +796,8 @@ def linear_w4a16(x, q, scales, d_s2, dtype=None, d_flags=None, stream=None):
 def _expert_weights(w, E: int, rows: int, cols: int, name: str) -> ExpertWeights:
     """(codes [E, rows, cols/2], scales [E, rows, cols/16], s2 [E]) of one matrix per expert."""
     q, sc, s2 = w
-    _u8(q, (E, rows, cols // 2), f"{name} codes")
-    _u8(sc, (E, rows, cols // 16), f"{name} scales")
-    return ExpertWeights(q.data_ptr(), sc.data_ptr(), _f32_n(s2, E, f"{name} s2"))
+    return ExpertWeights(_bytes(q, (E, rows, cols // 2), name), _bytes(sc, (E, rows, cols // 16), name),
+                         _f32_n(s2, E, name))
 
 
 def _routing(ids, weights, T: int):
@@ -819,29 +835,29 @@ def nv4_moe_work_bytes(T: int, top_k: int, H: int, I: int) -> int:
 
 def nv4_moe_route(x, w_router, ids, weights, renormalize=True, d_flags=None, stream=None):
     """ids, weights [T, top_k]: the experts of the largest router logits and their softmax weights."""
-    _here(x, w_router, ids, weights, d_flags)
+    dev = _here(x, w_router, ids, weights, d_flags)
     T, H, ldx = _rows16(x, "x")
     E, k = _router(w_router, x), _routing(ids, weights, T)
     _check(lib().nv4_moe_route(x.data_ptr(), _DT[x.dtype], T, H, ldx, w_router.data_ptr(), E, k, int(bool(renormalize)),
-                               ids.data_ptr(), weights.data_ptr(), _ptr(d_flags), _stream(stream)), "nv4_moe_route")
+                               ids.data_ptr(), weights.data_ptr(), _ptr(d_flags), _on(stream, dev)), "nv4_moe_route")
 
 
 def nv4_moe_experts(x, ids, weights, gate, up, down, out, work, d_flags=None, stream=None):
     """out[t] = sum_j weights[t, j] * down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j]; gate, up and
     down: (codes, scales, s2) of every expert's matrix; work: nv4_moe_work_bytes(T, top_k, H, I) bytes."""
-    _here(x, ids, weights, *gate, *up, *down, out, work, d_flags)
+    dev = _here(x, ids, weights, *gate, *up, *down, out, work, d_flags)
     k = _routing(ids, weights, x.shape[0])
     T, H, ldx, E, I, ldd = _moe_shapes(x, gate, down, out, work, k)
     g, u, d = (_expert_weights(gate, E, I, H, "gate"), _expert_weights(up, E, I, H, "up"),
                _expert_weights(down, E, H, I, "down"))
     _check(lib().nv4_moe_experts(x.data_ptr(), _DT[x.dtype], T, H, ldx, ids.data_ptr(), weights.data_ptr(), k, E, I,
                                  g, u, d, _DT[out.dtype], out.data_ptr(), ldd, work.data_ptr(),
-                                 work.numel() * work.element_size(), _ptr(d_flags), _stream(stream)), "nv4_moe_experts")
+                                 work.numel() * work.element_size(), _ptr(d_flags), _on(stream, dev)), "nv4_moe_experts")
 
 
 def nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize=True, d_flags=None, stream=None):
     """nv4_moe_route into ids and weights, then nv4_moe_experts."""
-    _here(x, w_router, *gate, *up, *down, ids, weights, out, work, d_flags)
+    dev = _here(x, w_router, *gate, *up, *down, ids, weights, out, work, d_flags)
     k = _routing(ids, weights, x.shape[0])
     T, H, ldx, E, I, ldd = _moe_shapes(x, gate, down, out, work, k)
     if _router(w_router, x) != E:
@@ -850,7 +866,7 @@ def nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormal
                _expert_weights(down, E, H, I, "down"))
     _check(lib().nv4_moe_layer(x.data_ptr(), _DT[x.dtype], T, H, ldx, w_router.data_ptr(), E, k, int(bool(renormalize)),
                                I, g, u, d, ids.data_ptr(), weights.data_ptr(), _DT[out.dtype], out.data_ptr(), ldd,
-                               work.data_ptr(), work.numel() * work.element_size(), _ptr(d_flags), _stream(stream)),
+                               work.data_ptr(), work.numel() * work.element_size(), _ptr(d_flags), _on(stream, dev)),
            "nv4_moe_layer")
 
 
@@ -895,22 +911,22 @@ def nv4_mxfp4_quant_mma(x, q, e8m0_mma, d_flags=None, stream=None):
     """MXFP4 of x [rows, cols] (bf16 or float32): codes [rows, cols/2] and scales in the MMA layout."""
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise NV4Error("x must be bf16 or float32")
-    _here(x, q, e8m0_mma, d_flags)
+    dev = _here(x, q, e8m0_mma, d_flags)
     rows, cols, ld = _rowmajor(x, "x")
-    _u8(q, (rows, cols // 2), "q")
+    _bytes(q, (rows, cols // 2), "q")
     _mma_bytes(e8m0_mma, rows, cols, "e8m0_mma")
     _check(lib().nv4_mxfp4_quant_mma(x.data_ptr(), _DT[x.dtype], rows, cols, max(ld, cols) if rows <= 1 else ld,
-                                     q.data_ptr(), e8m0_mma.data_ptr(), _ptr(d_flags), _stream(stream)),
+                                     q.data_ptr(), e8m0_mma.data_ptr(), _ptr(d_flags), _on(stream, dev)),
            "nv4_mxfp4_quant_mma")
 
 
 def nv4_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, out, d_flags=None, stream=None):
     """out[M, N] = A @ B^T for MXFP4 operands (codes [rows, K/2], E8M0 scales in the MMA layout)."""
-    _here(qa, sfa_mma, qb, sfb_mma, out, d_flags)
+    dev = _here(qa, sfa_mma, qb, sfb_mma, out, d_flags)
     M, half = qa.shape
     N, K = qb.shape[0], 2 * half
-    _u8(qa, (M, half), "qa")
-    _u8(qb, (N, half), "qb")
+    _bytes(qa, (M, half), "qa")
+    _bytes(qb, (N, half), "qb")
     _mma_bytes(sfa_mma, M, K, "sfa_mma")
     _mma_bytes(sfb_mma, N, K, "sfb_mma")
     if out.dtype not in (torch.bfloat16, torch.float32):
@@ -920,7 +936,7 @@ def nv4_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, out, d_flags=None, stream=None):
         raise NV4Error("out must be [M, N]")
     _check(lib().nv4_gemm_mxfp4(qa.data_ptr(), sfa_mma.data_ptr(), qb.data_ptr(), sfb_mma.data_ptr(), M, N, K,
                                 _DT[out.dtype], out.data_ptr(), max(ldd, N) if M <= 1 else ldd, _ptr(d_flags),
-                                _stream(stream)), "nv4_gemm_mxfp4")
+                                _on(stream, dev)), "nv4_gemm_mxfp4")
 
 
 def mxfp4_quant_mma(x, d_flags=None, stream=None):
@@ -937,8 +953,37 @@ def gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, dtype=torch.bfloat16, d_flags=None, str
     return out
 
 
+def nv4_linear_mxfp4_work_bytes(M: int, K: int) -> int:
+    return int(lib().nv4_linear_mxfp4_work_bytes(M, K))
+
+
+def nv4_linear_mxfp4(x, qw, sfw_mma, out, work, d_flags=None, stream=None):
+    """out[M, N] = Q(x) @ W^T: x [M, K] (bf16 or float32) quantized to MXFP4, MXFP4 weights (codes
+    [N, K/2], scales in the MMA layout); work: nv4_linear_mxfp4_work_bytes(M, K) bytes."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise NV4Error("x must be bf16 or float32")
+    dev = _here(x, qw, sfw_mma, out, work, d_flags)
+    M, K, ldx = _rowmajor(x, "x")
+    N = qw.shape[0]
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise NV4Error("out must be bf16 or float32")
+    orows, ocols, ldd = _rowmajor(out, "out")
+    if orows != M or ocols != N:
+        raise NV4Error("out must be [M, N]")
+    if not work.is_contiguous():
+        raise NV4Error("work must be contiguous")
+    _mma_bytes(sfw_mma, N, K, "sfw_mma")
+    _check(lib().nv4_linear_mxfp4(x.data_ptr(), _DT[x.dtype], M, K, max(ldx, K) if M <= 1 else ldx,
+                                  _bytes(qw, (N, K // 2), "qw"), sfw_mma.data_ptr(), N, _DT[out.dtype], out.data_ptr(),
+                                  max(ldd, N) if M <= 1 else ldd, work.data_ptr(), work.numel() * work.element_size(),
+                                  _ptr(d_flags), _on(stream, dev)), "nv4_linear_mxfp4")
+
+
 def linear_mxfp4(x, qw, sfw_mma, dtype=torch.bfloat16, d_flags=None, stream=None):
     """The W4A4 linear layer: x [M, K] quantized to MXFP4, times MXFP4 weights [N, K] (codes, scales
     in the MMA layout) -> [M, N]."""
-    q, sf = mxfp4_quant_mma(x, d_flags, stream)
-    return gemm_mxfp4(q, sf, qw, sfw_mma, dtype, d_flags, stream)
+    M, K = x.shape
+    out = _new((M, qw.shape[0]), dtype, x, stream)
+    work = _new((nv4_linear_mxfp4_work_bytes(M, K),), torch.uint8, x, stream)
+    nv4_linear_mxfp4(x, qw, sfw_mma, out, work, d_flags, stream)
+    return out

@@ -535,8 +535,8 @@ nv4_status nv4_mxfp4_quant_mma(const void* x, nv4_dtype dt, int64_t rows, int64_
                                             (cudaStream_t)stream));
 }
 
-nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8_t* qb, const uint8_t* sfb_mma, int64_t M,
-                          int64_t N, int64_t K, nv4_dtype out_dt, void* out, int64_t ldd, uint32_t* d_flags, void* stream)
+static nv4_status check_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8_t* qb, const uint8_t* sfb_mma,
+                                   int64_t M, int64_t N, int64_t K, nv4_dtype out_dt, const void* out, int64_t ldd)
 {
     if (out_dt != NV4_BF16 && out_dt != NV4_FP32) return NV4_ERR_DTYPE;
     if (M < 0 || N < 0 || K < 0 || K % 32 != 0 || ldd < N) return NV4_ERR_SHAPE;
@@ -547,7 +547,37 @@ nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8
     if (M >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 31 ||
         ((M + 255) / 256) * ((N + 255) / 256) >= (int64_t)1 << 31)
         return NV4_ERR_LIMIT;
-    return from_cuda(launch_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, M, N, K, (int)out_dt, out, ldd, d_flags,
+    return NV4_OK;
+}
+
+nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8_t* qb, const uint8_t* sfb_mma, int64_t M,
+                          int64_t N, int64_t K, nv4_dtype out_dt, void* out, int64_t ldd, uint32_t* d_flags, void* stream)
+{
+    const nv4_status st = check_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, M, N, K, out_dt, out, ldd);
+    if (st != NV4_OK || M == 0 || N == 0) return st;
+    return from_cuda(launch_gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, M, N, K, (int)out_dt, out, ldd, false, d_flags,
+                                       (cudaStream_t)stream));
+}
+
+size_t nv4_linear_mxfp4_work_bytes(int64_t M, int64_t K)
+{
+    const size_t sf = nv4_mxfp4_mma_scale_bytes(M, K);             // 0 for sizes that are refused
+    return sf == 0 ? 0 : sf + (size_t)M * (size_t)(K / 2);
+}
+
+nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
+                            const uint8_t* sfw_mma, int64_t N, nv4_dtype out_dt, void* out, int64_t ldd, void* d_work,
+                            size_t work_bytes, uint32_t* d_flags, void* stream)
+{
+    uint8_t* sf = static_cast<uint8_t*>(d_work);                   // a multiple of 512 bytes
+    uint8_t* q = sf == nullptr ? nullptr : sf + nv4_mxfp4_mma_scale_bytes(M, K);
+    if (M > 0 && N > 0 && K > 0 && K % 32 == 0 && d_work != nullptr && work_bytes < nv4_linear_mxfp4_work_bytes(M, K))
+        return NV4_ERR_LIMIT;
+    nv4_status st = check_gemm_mxfp4(q, sf, qw, sfw_mma, M, N, K, out_dt, out, ldd);
+    if (st != NV4_OK || M == 0 || N == 0) return st;
+    st = nv4_mxfp4_quant_mma(x, dt, M, K, ldx, q, sf, d_flags, stream);
+    if (st != NV4_OK) return st;
+    return from_cuda(launch_gemm_mxfp4(q, sf, qw, sfw_mma, M, N, K, (int)out_dt, out, ldd, true, d_flags,
                                        (cudaStream_t)stream));
 }
 

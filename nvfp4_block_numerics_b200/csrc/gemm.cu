@@ -811,10 +811,12 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa, const float
 }
 
 cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
-                              int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,
-                              cudaStream_t s)
+                              int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, bool dependent,
+                              uint32_t* d_flags, cudaStream_t s)
 {
     using namespace gemm;
+    // few rows: the rows of B fill the tensor cores' 128 rows (gemm_mx.cu)
+    if (M <= 128) return launch_gemm_mxfp4_small(qa, sfa, qb, sfb, M, N, K, out_dt, out, ldd, dependent, d_flags, s);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -118,9 +118,13 @@ cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_
 cudaError_t launch_moe_experts(const MoeExpertsArgs& a, bool routed, cudaStream_t s);
 cudaError_t launch_mxfp4_quant_mma(const void* x, int in_dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
                                    uint8_t* sf, uint32_t* d_flags, cudaStream_t s);
+// dependent: the call in front on the stream is launch_mxfp4_quant_mma, which wrote qa and sfa.
 cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
-                              int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,
-                              cudaStream_t s);
+                              int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, bool dependent,
+                              uint32_t* d_flags, cudaStream_t s);
+cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
+                                    int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, bool dependent,
+                                    uint32_t* d_flags, cudaStream_t s);
 cudaError_t launch_dequant(const DequantTask* tasks, int n, int out_dt, cudaStream_t s);
 cudaError_t launch_hessian(const nv4_hessian_job* jobs, int n, uint32_t* d_flags, cudaStream_t s, int* bad_job);
 cudaError_t launch_sweep(const nv4_sweep_job* jobs, int n, int dt, uint32_t* d_flags, cudaStream_t s);

@@ -123,6 +123,7 @@ mxfp4_quant_mma_kernel(const void* x, uint32_t rows, uint32_t cols, uint32_t kt,
                        uint32_t* __restrict__ d_flags)
 {
     const uint32_t lane = threadIdx.x & 31u, hpr = kt * 8u;       // half blocks per padded row
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product may start (and waits for this grid)
     uint32_t flags = 0u;
     // total = padded rows x hpr is a multiple of 32: every warp is whole
     for (uint32_t h = blockIdx.x * kVarThreads + threadIdx.x; h < total; h += gridDim.x * kVarThreads) {

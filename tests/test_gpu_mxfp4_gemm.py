@@ -150,9 +150,14 @@ def test_linear_mxfp4_run(orc):
         with torch.cuda.graph(graph):
             nv4.nv4_mxfp4_quant_mma(xin, q, sf)
             nv4.nv4_gemm_mxfp4(q, sf, dq, ds, out)
+        work = torch.full((nv4.nv4_linear_mxfp4_work_bytes(M, 736),), 0xFF, dtype=torch.uint8, device=G.DEV)
+        graph2, out2 = torch.cuda.CUDAGraph(), torch.empty_like(out)
+        with torch.cuda.graph(graph2):
+            nv4.nv4_linear_mxfp4(xin, dq, ds, out2, work)
         for x, y in zip(xs, want):
             xin.copy_(x)
             graph.replay()
+            graph2.replay()
             torch.cuda.synchronize()
-            assert torch.equal(out, y)
+            assert torch.equal(out, y) and torch.equal(out2, y)
     assert nv4.linear_mxfp4(xs[0][:0], dq, ds).shape == (0, 520)

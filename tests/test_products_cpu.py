@@ -112,6 +112,14 @@ def test_mxfp4_product_refusals(L):
     assert gemm(qa=None) == 1 and gemm(sb=None) == 1 and gemm(out=None) == 1
     assert gemm(qb=FAKE + 8) == 3 and gemm(sa=FAKE + 4) == 3 and gemm(out=FAKE + 8) == 3
     assert gemm(M=0) == 0 and gemm(N=0, ldd=0) == 0 and gemm(M=1 << 31) == 6
+
+    def linear(x=FAKE, dt=0, M=4, K=64, ldx=64, qw=FAKE, sw=FAKE, N=8, odt=0, out=FAKE, ldd=8, work=FAKE, wb=1 << 20):
+        return L.nv4_linear_mxfp4(x, dt, M, K, ldx, qw, sw, N, odt, out, ldd, work, wb, None, None)
+
+    assert linear(dt=1) == 4 and linear(odt=1) == 4 and linear(K=48, ldx=48) == 2 and linear(ldx=32) == 2
+    assert linear(x=None) == 1 and linear(qw=None) == 1 and linear(work=None) == 1 and linear(out=FAKE + 8) == 3
+    assert linear(work=FAKE + 8) == 3 and linear(wb=L.nv4_linear_mxfp4_work_bytes(4, 64) - 1) == 6 and linear(M=0) == 0
+    assert L.nv4_linear_mxfp4_work_bytes(4, 64) == 512 + 4 * 32 and L.nv4_linear_mxfp4_work_bytes(0, 64) == 0
     assert L.nv4_mxfp4_mma_scale_bytes(200, 288) == 256 * 12 and L.nv4_mxfp4_mma_scale_bytes(1, 32) == 512
     assert L.nv4_mxfp4_mma_scale_bytes(4, 48) == 0 and L.nv4_mxfp4_mma_scale_bytes(0, 32) == 0
 
