@@ -14,9 +14,9 @@
 //     exact logits whatever the summation order.  It also converts BF16 token rows to FP16, each
 //     with a power of two of its own (moe_rows_kernel does where the experts are given).
 //   * moe_up_kernel, one CTA per SM: the flat list (expert, i) of gate / up row pairs of the
-//     chosen experts is cut into one contiguous range per CTA, walked in tiles of 8 pairs: MMA
-//     rows 0-7 are gate rows, 8-15 the same up rows, so both halves of an h meet in one thread.
-//     h goes to the workspace in FP32.
+//     chosen experts is cut into one contiguous range per CTA, walked in tiles of 16 pairs, two
+//     MMA row groups of 8 gate rows and the same 8 up rows, so both halves of an h meet in one
+//     thread.  h goes to the workspace in FP32.
 //   * moe_hidden_kernel, one CTA per (expert, token) row of h: scales it by a power of two and
 //     rounds it to FP16 (11 bits: a relative error of 2^-11, an eighth of the BF16 output's own).
 //   * moe_down_kernel, one CTA per SM: a CTA owns a range of output rows for all tokens and all
@@ -385,9 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     extern __shared__ __align__(16) uint8_t smem[];                // the warps' rings
     __shared__ Lists L;
     __shared__ Segs S;
-    __shared__ __align__(16) float red[2][kWarps][16 * 8];
+    __shared__ __align__(16) float red[kWarps][32 * 8];            // [half][gate 8, up 8][column]
     __shared__ float descale[kMaxMoeTokens];
-    constexpr uint32_t kTile = 16u * 8u;
+    constexpr uint32_t kTile = 32u * 8u;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const uint32_t nch = (p.H + kChunk - 1u) / kChunk;
     w4::pdl_wait();                                                // ids are the router's
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
                 sg.m = min(kPass, L.first[a + 1u] - sg.f0);
                 sg.i0 = w - s * p.I;
                 sg.n = min(p.I - sg.i0, end - w);
-                const uint32_t tiles = (sg.n + 7u) / 8u;
+                const uint32_t tiles = (sg.n + 15u) / 16u;
                 sg.th = (sg.n + tiles - 1u) / tiles;
                 sg.tile0 = nt;
                 sg.sg = __ldg(p.g2 + sg.expert);
@@ -432,19 +432,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
         const uint32_t my_tiles = grp < S.ntile ? (S.ntile - grp + groups - 1u) / groups : 0u;
         const uint32_t steps = my_tiles * (wig < nch ? (nch - wig + wk - 1u) / wk : 0u);
         uint32_t lt = grp, lc = wig, ls = 0u;
-        w4::Rows16 rw;
+        w4::Rows16 rw[2];
         bool moved = true;
         auto load = [&](uint8_t* slot) {
             if (moved) {
                 while (ls + 1u < S.n && lt >= S.s[ls + 1u].tile0) ++ls;
                 const Seg& sg = S.s[ls];
-                const uint32_t i = (lt - sg.tile0) * sg.th + g;
-                const bool live = g < sg.th && i < sg.n;
-                const size_t row = ((size_t)sg.expert * p.I + sg.i0 + i) * (p.H / 2u);
-                rw.set(p.gq + row, p.gs + row / 8u, p.uq + row, p.us + row / 8u, live, live);
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    const uint32_t r = 8u * h + g, i = (lt - sg.tile0) * sg.th + r;
+                    const bool live = r < sg.th && i < sg.n;
+                    const size_t row = ((size_t)sg.expert * p.I + sg.i0 + i) * (p.H / 2u);
+                    rw[h].set(p.gq + row, p.gs + row / 8u, p.uq + row, p.us + row / 8u, live, live);
+                }
                 moved = false;
             }
-            w4::load_chunk<kVec>(slot, rw, lc, p.H);
+            w4::load_chunk<kVec>(slot, rw[0], lc, p.H);
+            w4::load_chunk<kVec>(slot + w4::kSlot, rw[1], lc, p.H);
             lc += wk;
             if (lc >= nch) {
                 lc = wig;
@@ -452,36 +456,40 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
                 moved = true;
             }
         };
-        w4::Ring ring;
-        ring.begin(smem + warp * (w4::kDepth * w4::kSlot), steps, load);
-        w4::Acc<1> acc;
-        w4::clear<1>(acc);
-        uint32_t ut = grp, uc = wig, us = 0u, buf = 0u;
+        w4::Ring32 ring;
+        ring.begin(smem + warp * (w4::kDepth32 * 2u * w4::kSlot), steps, load);
+        w4::AccOf<1, 2> acc[2];
+        w4::clear<1, 2>(acc[0]);
+        w4::clear<1, 2>(acc[1]);
+        uint32_t ut = grp, uc = wig, us = 0u;
         const uint16_t* xr = nullptr;                              // column g's token row
         ring.run(load, [&](const uint8_t* slot) {
             if (uc == wig) {
                 while (us + 1u < S.n && ut >= S.s[us + 1u].tile0) ++us;
                 xr = x + (int64_t)L.tok[S.s[us].f0 + min(g, S.s[us].m - 1u)] * ldx;
             }
-            if (wide) w4::mma_chunk_global<true>(acc, slot, xr, uc, p.H);
-            else w4::mma_chunk_global<false>(acc, slot, xr, uc, p.H);
+            if (wide) w4::mma_rows<true, 2, 2>(acc, slot, xr, uc, p.H);
+            else w4::mma_rows<false, 2, 2>(acc, slot, xr, uc, p.H);
             uc += wk;
             if (uc < nch) return;
-            w4::put_part<1>(red[buf][warp], acc, g, t);
-            w4::clear<1>(acc);
+            w4::group_barrier(grp, wk);                            // the last tile's sums have been read
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w4::put_part<1, 2>(red[warp] + 16 * 8 * h, acc[h], g, t);
+                w4::clear<1, 2>(acc[h]);
+            }
             w4::group_barrier(grp, wk);
             const Seg& sg = S.s[us];
             const uint32_t a = (ut - sg.tile0) * sg.th, nr = min(sg.th, sg.n - a);
-            const float* first = red[buf][grp * wk];
-            for (uint32_t i = wig * 32u + lane; i < 8u * sg.m; i += 32u * wk) {
-                const uint32_t r = i & 7u, col = i >> 3, hr = sg.f0 + col;
+            const float* first = red[grp * wk];
+            for (uint32_t i = wig * 32u + lane; i < 16u * sg.m; i += 32u * wk) {
+                const uint32_t r = i & 15u, col = i >> 4, hr = sg.f0 + col, at_r = (r >> 3) * 128u + (r & 7u) * 8u + col;
                 if (r >= nr) continue;
                 const float ds = descale[L.tok[hr]];
-                const float gv = w4::sum_parts<kTile>(first + r * 8u + col, wk) * sg.sg * ds;
-                const float uv = w4::sum_parts<kTile>(first + (r + 8u) * 8u + col, wk) * sg.su * ds;
+                const float gv = w4::sum_parts<kTile>(first + at_r, wk) * sg.sg * ds;
+                const float uv = w4::sum_parts<kTile>(first + at_r + 64u, wk) * sg.su * ds;
                 p.work.h[(size_t)hr * p.I + sg.i0 + a + r] = gv / (1.0f + expf(-gv)) * uv;
             }
-            buf ^= 1u;
             uc = wig;
             ut += groups;
         });
@@ -612,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     __syncthreads();                                               // coef
     for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) coef[i] *= p.work.hd[i];
     __syncthreads();
-    w4::Acc<1> acc;
-    w4::clear<1>(acc);
+    w4::Acc<1> acc[1];
+    w4::clear<1>(acc[0]);
     uint32_t left = steps, f0 = 0u, m = 0u;
     const uint16_t* xr = nullptr;
     bool fresh = true;
@@ -625,22 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             xr = p.work.h16 + (size_t)(f0 + min(g, m - 1u)) * w4::padded(p.I);
             fresh = false;
         }
-        w4::mma_chunk_global<false>(acc, slot, xr, uc, p.I);
+        w4::mma_rows<false, 1, 4>(acc, slot, xr, uc, p.I);
         --left;
         if (++uc < nch && left != 0u) return;
         // the sub-list's end: its columns, each times its coefficient, into the warp's sums
-        w4::join<1>(acc);
+        w4::join<1>(acc[0]);
 #pragma unroll
         for (uint32_t i = 0; i < 2; ++i) {
             const uint32_t col = 2u * t + i;
             if (col < m) {
                 float* y = Y + (size_t)L.tok[f0 + col] * 16u;
-                y[g] += acc[0][0][i] * coef[f0 + col];
-                y[g + 8] += acc[0][0][2 + i] * coef[f0 + col];
+                y[g] += acc[0][0][0][i] * coef[f0 + col];
+                y[g + 8] += acc[0][0][0][2 + i] * coef[f0 + col];
             }
         }
         __syncwarp();
-        w4::clear<1>(acc);
+        w4::clear<1>(acc[0]);
         uc = 0u;
         ++us;
         fresh = true;
@@ -711,9 +719,9 @@ template <bool kVec>
 static cudaError_t run_up(const Experts& p, cudaStream_t s)
 {
     static bool ready[64] = {};
-    const cudaError_t e = prepare(moe_up_kernel<kVec>, ready, (int)w4::kRing, false);
+    const cudaError_t e = prepare(moe_up_kernel<kVec>, ready, (int)w4::kRing32, false);
     if (e != cudaSuccess) return e;
-    return launch(moe_up_kernel<kVec>, p, (uint32_t)num_sms(), kThreads, w4::kRing, 1u, true, s);
+    return launch(moe_up_kernel<kVec>, p, (uint32_t)num_sms(), kThreads, w4::kRing32, 1u, true, s);
 }
 
 template <int kOut, bool kVec>

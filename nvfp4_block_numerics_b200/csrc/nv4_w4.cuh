@@ -36,9 +36,11 @@ namespace w4 {
 constexpr int kThreads = 512;                     // 16 warps, one CTA per SM
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kChunk = 256;                  // K-elements of one warp step
-constexpr int kDepth = 3;                         // chunks in flight per warp
+constexpr int kDepth = 3;                         // chunks of 16 rows in flight per warp
+constexpr int kDepth32 = 2;                       // chunks of 2 x 16 rows
 constexpr uint32_t kSlot = 16u * 128u + 16u * 16u;          // codes and scales of 16 rows x 256
 constexpr uint32_t kRing = kWarps * kDepth * kSlot;         // bytes for all warps
+constexpr uint32_t kRing32 = kWarps * kDepth32 * 2u * kSlot;
 
 // Copies n of kBytes (0 or kBytes) bytes and fills up with zeros.
 template <int kBytes>
@@ -120,8 +122,9 @@ __device__ __forceinline__ void load_chunk(uint8_t* slot, const Rows16& r, uint3
 
 // Walks a warp's steps: load(slot) starts the next step's loads, use(slot) multiplies the next
 // one.  begin() before the token rows are staged, run() after.
-struct Ring {
-    uint8_t* base;                                // this warp's kDepth slots
+template <int kSlots, uint32_t kBytes>
+struct RingOf {
+    uint8_t* base;                                // this warp's slots
     uint32_t steps, issued;
 
     template <class Load>
@@ -130,8 +133,8 @@ struct Ring {
         base = b;
         steps = n;
         issued = 0u;
-        for (int i = 0; i < kDepth; ++i) {
-            if (issued < steps) load(base + issued * kSlot);
+        for (int i = 0; i < kSlots; ++i) {
+            if (issued < steps) load(base + issued * kBytes);
             ++issued;
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -142,19 +145,21 @@ struct Ring {
     {
         uint32_t at = 0u;
         for (uint32_t i = 0; i < steps; ++i) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
             __syncwarp();
-            uint8_t* slot = base + at * kSlot;
+            uint8_t* slot = base + at * kBytes;
             use(slot);
             __syncwarp();                         // the slot has been read
             if (issued < steps) load(slot);
             ++issued;
             asm volatile("cp.async.commit_group;" ::: "memory");
-            at = at + 1u == (uint32_t)kDepth ? 0u : at + 1u;
+            at = at + 1u == (uint32_t)kSlots ? 0u : at + 1u;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 };
+using Ring = RingOf<kDepth, kSlot>;
+using Ring32 = RingOf<kDepth32, 2u * kSlot>;
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
@@ -204,13 +209,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 template <int NT>
 constexpr int kChains = NT == 1 ? 4 : NT == 2 ? 2 : 1;
 
+template <int NT, int kCh>
+using AccOf = float[kCh][NT][4];
 template <int NT>
 using Acc = float[kChains<NT>][NT][4];
 
 // acc += 16 weight rows x token rows over one chunk.  x(j, u): this lane's 16-byte vector of token
 // 8 j + g, the 8 elements from 128 (u / 4) + 32 t + 8 (u % 4) of the chunk on.
-template <bool kWide, int NT, class X>
-__device__ __forceinline__ void mma_step(Acc<NT>& acc, const uint8_t* slot, X x)
+template <bool kWide, int NT, int kCh, class X>
+__device__ __forceinline__ void mma_step(AccOf<NT, kCh>& acc, const uint8_t* slot, X x)
 {
     const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
 #pragma unroll
@@ -238,8 +245,8 @@ __device__ __forceinline__ void mma_step(Acc<NT>& acc, const uint8_t* slot, X x)
 #pragma unroll
             for (uint32_t j = 0; j < (uint32_t)NT; ++j) {
                 const uint4 v = x(j, 4u * p + u);
-                mma<kWide>(acc[(2u * u) % kChains<NT>][j], a[0], b[0], a[1], b[1], v.x, v.y);
-                mma<kWide>(acc[(2u * u + 1u) % kChains<NT>][j], a[2], b[2], a[3], b[3], v.z, v.w);
+                mma<kWide>(acc[(2u * u) % kCh][j], a[0], b[0], a[1], b[1], v.x, v.y);
+                mma<kWide>(acc[(2u * u + 1u) % kCh][j], a[2], b[2], a[3], b[3], v.z, v.w);
             }
         }
     }
@@ -254,17 +261,18 @@ __device__ __forceinline__ void mma_chunk(Acc<NT>& acc, const uint8_t* slot, con
     const uint4* x0[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) x0[j] = xs + (8u * j + g < m ? 8u * j + g : 0u) * 4u + t;
-    mma_step<kWide, NT>(acc, slot, [&](uint32_t j, uint32_t u) { return x0[j][u * m * 4u]; });
+    mma_step<kWide, NT, kChains<NT>>(acc, slot, [&](uint32_t j, uint32_t u) { return x0[j][u * m * 4u]; });
 }
 
-// Up to 8 token rows in global memory.  row: this lane's (column g's), chunk: where the step begins.
-// kWide: BF16 as the caller gave it, K elements.  Else FP16 in vector order, zero-padded to whole
-// chunks: the 32 vectors of a chunk as [u][t], so that the four lanes of a column read 64
+// Up to 8 token rows in global memory against kHalves groups of 16 weight rows (slot, slot + kSlot),
+// which share what is loaded of the tokens.  row: this lane's (column g's), chunk: where the step
+// begins.  kWide: BF16 as the caller gave it, K elements.  Else FP16 in vector order, zero-padded to
+// whole chunks: the 32 vectors of a chunk as [u][t], so that the four lanes of a column read 64
 // consecutive bytes (in the natural order they touch four places 64 bytes apart, and L1 was what
 // bounded the gate / up product of 48 tokens: 85% busy, 176 us).
-template <bool kWide>
-__device__ __forceinline__ void mma_chunk_global(Acc<1>& acc, const uint8_t* slot, const uint16_t* row, uint32_t chunk,
-                                                 uint32_t K)
+template <bool kWide, int kHalves, int kCh>
+__device__ __forceinline__ void mma_rows(AccOf<1, kCh> (&acc)[kHalves], const uint8_t* slot, const uint16_t* row, uint32_t chunk,
+                                         uint32_t K)
 {
     const uint32_t t = threadIdx.x & 3u;
     uint4 v[8];
@@ -277,7 +285,9 @@ __device__ __forceinline__ void mma_chunk_global(Acc<1>& acc, const uint8_t* slo
             v[u] = *reinterpret_cast<const uint4*>(row + chunk * kChunk + 32u * u + 8u * t);
         }
     }
-    mma_step<kWide, 1>(acc, slot, [&](uint32_t, uint32_t u) { return v[u]; });
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+        mma_step<kWide, 1, kCh>(acc[h], slot + h * kSlot, [&](uint32_t, uint32_t u) { return v[u]; });
 }
 
 // Element offset, in a row in vector order, of the 8 values from 8 v on.
@@ -455,21 +465,21 @@ __device__ __forceinline__ float sum_parts(const float* first, uint32_t wk)
     return s;
 }
 
-template <int NT>
-__device__ __forceinline__ void clear(Acc<NT>& acc)
+template <int NT, int kCh = kChains<NT>>
+__device__ __forceinline__ void clear(AccOf<NT, kCh>& acc)
 {
 #pragma unroll
-    for (int c = 0; c < kChains<NT>; ++c)
+    for (int c = 0; c < kCh; ++c)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[c][j][0] = acc[c][j][1] = acc[c][j][2] = acc[c][j][3] = 0.0f;
 }
 
 // The chains' sum, in chain (0).
-template <int NT>
-__device__ __forceinline__ void join(Acc<NT>& acc)
+template <int NT, int kCh = kChains<NT>>
+__device__ __forceinline__ void join(AccOf<NT, kCh>& acc)
 {
 #pragma unroll
-    for (int c = kChains<NT> / 2; c > 0; c /= 2)
+    for (int c = kCh / 2; c > 0; c /= 2)
 #pragma unroll
         for (int i = 0; i < c; ++i)
 #pragma unroll
@@ -479,10 +489,10 @@ __device__ __forceinline__ void join(Acc<NT>& acc)
 }
 
 // A warp's 16 x 8 NT sums to its place in shared memory, [16][8 NT].
-template <int NT>
-__device__ __forceinline__ void put_part(float* part, Acc<NT>& chains, uint32_t g, uint32_t t)
+template <int NT, int kCh = kChains<NT>>
+__device__ __forceinline__ void put_part(float* part, AccOf<NT, kCh>& chains, uint32_t g, uint32_t t)
 {
-    join<NT>(chains);
+    join<NT, kCh>(chains);
     const float (&acc)[NT][4] = chains[0];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
