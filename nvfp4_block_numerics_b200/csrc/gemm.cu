@@ -154,7 +154,7 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
                 const uint32_t n_tile = t % p.n_tiles, m_tile = t / p.n_tiles;
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages;
-                    if (g >= (uint32_t)kStages && !mbar_wait(&sm.empty[s], ((g / kStages) - 1u) & 1u)) {
+                    if (g >= (uint32_t)kStages && !wait_bar(&sm.empty[s], ((g / kStages) - 1u) & 1u)) {
                         flags |= kFlagTimeout;
                         atomicOr(&sm.abort, 1u);
                     }
@@ -178,7 +178,7 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
             uint32_t g = 0, i = 0;
             for (uint32_t t = blockIdx.x; t < p.tiles && !aborted(); t += gridDim.x, ++i) {
                 // the accumulator is free once the epilogue has read the previous tile
-                if (i > 0 && !mbar_wait(&sm.acc_empty, (i - 1u) & 1u)) {
+                if (i > 0 && !wait_bar(&sm.acc_empty, (i - 1u) & 1u)) {
                     flags |= kFlagTimeout;
                     atomicOr(&sm.abort, 1u);
                     break;
@@ -187,8 +187,8 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages;
                     const uint32_t b = g % kSfBufs;
-                    if (!mbar_wait(&sm.full[s], (g / kStages) & 1u) ||
-                        !mbar_wait(&sm.sf_full[b], (g / kSfBufs) & 1u)) {
+                    if (!wait_bar(&sm.full[s], (g / kStages) & 1u) ||
+                        !wait_bar(&sm.sf_full[b], (g / kSfBufs) & 1u)) {
                         flags |= kFlagTimeout;
                         atomicOr(&sm.abort, 1u);
                         break;
@@ -211,7 +211,7 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
             }
             sm.consumed = g;
             tc_commit(&sm.drain);                                  // every tensor-core operation issued
-            if (!mbar_wait(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
@@ -230,8 +230,8 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
         for (uint32_t t = blockIdx.x; t < p.tiles && !quit; t += gridDim.x) {
             for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                 const uint32_t s = g % kStages, b = g % kSfBufs;
-                bool ok = mbar_wait(&sm.full[s], (g / kStages) & 1u);
-                if (ok && g >= (uint32_t)kSfBufs) ok = mbar_wait(&sm.sf_free[b], ((g / kSfBufs) - 1u) & 1u);
+                bool ok = wait_bar(&sm.full[s], (g / kStages) & 1u);
+                if (ok && g >= (uint32_t)kSfBufs) ok = wait_bar(&sm.sf_free[b], ((g / kSfBufs) - 1u) & 1u);
                 const bool timed_out = __any_sync(0xFFFFFFFFu, !ok);
                 quit = timed_out || __any_sync(0xFFFFFFFFu, aborted());
                 if (quit) {
@@ -274,7 +274,7 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
         constexpr int kChunks = kBN / 64;                          // 32-column chunks per warp
         uint32_t i = 0;
         for (uint32_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++i) {
-            const bool ok = !aborted() && mbar_wait(&sm.acc_full, i & 1u);
+            const bool ok = !aborted() && wait_bar(&sm.acc_full, i & 1u);
             if (!ok) {
                 if (!aborted()) { flags |= kFlagTimeout; atomicOr(&sm.abort, 1u); }
                 break;
@@ -343,7 +343,7 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
     __syncthreads();
     if (threadIdx.x == kProducer) {
         for (uint32_t g = sm.consumed; g < sm.issued; ++g)
-            if (!mbar_wait(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
     }
     if (warp == kIssuer / 32) {
         tc_fence_after();
@@ -435,7 +435,7 @@ gemm_pair_kernel(const __grid_constant__ Params p)
                 const uint32_t mrow = 2u * m_tile + rank, nrow = 2u * n_tile + rank;   // 128-row tiles
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages;
-                    if (g >= (uint32_t)kStages && !mbar_wait(&sm.empty[s], ((g / kStages) - 1u) & 1u)) give_up();
+                    if (g >= (uint32_t)kStages && !wait_bar(&sm.empty[s], ((g / kStages) - 1u) & 1u)) give_up();
                     if (aborted()) break;
                     mbar_arrive_expect_tx(&sm.full[s], kTx);
                     tma_load_2d(sm.a[s], &p.map_a, &sm.full[s], (int)(ks * 128u), (int)(mrow * 128u));
@@ -469,15 +469,15 @@ gemm_pair_kernel(const __grid_constant__ Params p)
         if (lane == 0 && rank == 0) {                              // the pair's MMA issuer
             uint32_t g = 0, i = 0;
             for (uint32_t t = pair; t < p.tiles && !aborted(); t += npairs, ++i) {
-                if (i > 0 && !mbar_wait(&sm.acc_empty, (i - 1u) & 1u)) {
+                if (i > 0 && !wait_bar(&sm.acc_empty, (i - 1u) & 1u)) {
                     give_up();
                     break;
                 }
                 tc_fence_after();
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages, b = g % kSfBufs2, ph = (g / kStages) & 1u;
-                    if (!mbar_wait(&sm.full[s], ph) || !mbar_wait(&sm.sf_full[b], (g / kSfBufs2) & 1u) ||
-                        !mbar_wait(&sm.peer_ready[s], ph)) {
+                    if (!wait_bar(&sm.full[s], ph) || !wait_bar(&sm.sf_full[b], (g / kSfBufs2) & 1u) ||
+                        !wait_bar(&sm.peer_ready[s], ph)) {
                         give_up();
                         break;
                     }
@@ -500,13 +500,13 @@ gemm_pair_kernel(const __grid_constant__ Params p)
             }
             sm.consumed = g;
             tc_commit_pair(&sm.drain);
-            if (!mbar_wait(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
         } else if (lane == 0) {                                    // rank 1: forwards its landed stages
             uint32_t g = 0;
             for (uint32_t t = pair; t < p.tiles && !aborted(); t += npairs) {
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages;
-                    if (!mbar_wait(&sm.full[s], (g / kStages) & 1u)) {
+                    if (!wait_bar(&sm.full[s], (g / kStages) & 1u)) {
                         give_up();
                         break;
                     }
@@ -524,8 +524,8 @@ gemm_pair_kernel(const __grid_constant__ Params p)
         for (uint32_t t = pair; t < p.tiles && !quit; t += npairs) {
             for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                 const uint32_t s = g % kStages, b = g % kSfBufs2;
-                bool ok = mbar_wait(&sm.full[s], (g / kStages) & 1u);
-                if (ok && g >= (uint32_t)kSfBufs2) ok = mbar_wait(&sm.sf_free[b], ((g / kSfBufs2) - 1u) & 1u);
+                bool ok = wait_bar(&sm.full[s], (g / kStages) & 1u);
+                if (ok && g >= (uint32_t)kSfBufs2) ok = wait_bar(&sm.sf_free[b], ((g / kSfBufs2) - 1u) & 1u);
                 const bool timed_out = __any_sync(0xFFFFFFFFu, !ok);
                 quit = timed_out || __any_sync(0xFFFFFFFFu, aborted());
                 if (quit) {
@@ -573,7 +573,7 @@ gemm_pair_kernel(const __grid_constant__ Params p)
         };
         uint32_t i = 0;
         for (uint32_t t = pair; t < p.tiles; t += npairs, ++i) {
-            const bool ok = !aborted() && mbar_wait(&sm.acc_full, i & 1u);
+            const bool ok = !aborted() && wait_bar(&sm.acc_full, i & 1u);
             if (!ok) {
                 if (!aborted()) give_up();
                 break;
@@ -659,7 +659,7 @@ gemm_pair_kernel(const __grid_constant__ Params p)
     __syncthreads();
     if (threadIdx.x == kProducer) {
         for (uint32_t g = sm.consumed; g < sm.issued; ++g)
-            if (!mbar_wait(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
     }
     tc_fence_before();
     cluster_sync();

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
             for (uint32_t ks = 0; ks < first; ++ks) rows(ks);
             uint32_t ks = first;
             for (; ks < KS; ++ks) {
-                if (!mbar_wait(&sm.empty[ks % kStages], ((ks / kStages) - 1u) & 1u)) give_up();
+                if (!wait_bar(&sm.empty[ks % kStages], ((ks / kStages) - 1u) & 1u)) give_up();
                 if (aborted()) break;
                 weights(ks);
                 rows(ks);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
             uint32_t ks = 0;
             for (; ks < KS; ++ks) {
                 const uint32_t s = ks % kStages, b = ks % kSfBufs;
-                if (!mbar_wait(&sm.full[s], (ks / kStages) & 1u) || !mbar_wait(&sm.sf_full[b], (ks / kSfBufs) & 1u)) {
+                if (!wait_bar(&sm.full[s], (ks / kStages) & 1u) || !wait_bar(&sm.sf_full[b], (ks / kSfBufs) & 1u)) {
                     give_up();
                     break;
                 }
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
             sm.consumed = ks;
             if (ks == KS) tc_commit(&sm.acc_full);
             tc_commit(&sm.drain);
-            if (!mbar_wait(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
         bool quit = false;
         for (uint32_t ks = 0; ks < KS; ++ks) {
             const uint32_t s = ks % kStages, b = ks % kSfBufs;
-            bool ok = mbar_wait(&sm.full[s], (ks / kStages) & 1u);
-            if (ok && ks >= (uint32_t)kSfBufs) ok = mbar_wait(&sm.sf_free[b], ((ks / kSfBufs) - 1u) & 1u);
+            bool ok = wait_bar(&sm.full[s], (ks / kStages) & 1u);
+            if (ok && ks >= (uint32_t)kSfBufs) ok = wait_bar(&sm.sf_free[b], ((ks / kSfBufs) - 1u) & 1u);
             const bool timed_out = __any_sync(0xFFFFFFFFu, !ok);
             quit = timed_out || __any_sync(0xFFFFFFFFu, aborted());
             if (quit) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
         }
         // the accumulator, transposed into shared memory: [row of A][128 weight rows]
         if (!quit) {
-            const bool ok = mbar_wait(&sm.acc_full, 0u);
+            const bool ok = wait_bar(&sm.acc_full, 0u);
             if (__any_sync(0xFFFFFFFFu, !ok)) {
                 if (lane == 0) give_up();
             } else {
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
     __syncthreads();
     if (threadIdx.x == 0)
         for (uint32_t ks = sm.consumed; ks < sm.issued; ++ks)
-            if (!mbar_wait(&sm.full[ks % kStages], (ks / kStages) & 1u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.full[ks % kStages], (ks / kStages) & 1u)) flags |= kFlagTimeout;
     if (p.z > 1u) cluster_sync();
     if (!aborted()) {
         const uint32_t n0 = n_tile * 128u, rows = min(128u, p.N - n0), toks = min((uint32_t)kTok, p.M - m0);

@@ -7,6 +7,28 @@ namespace nv4 {
 namespace tc {
 
 // ---------------------------------------------------------------- PTX helpers
+// As mbar_wait (false when the phase did not complete within kWaitLimitNs), with a time for which
+// the hardware may suspend the thread.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity)
+{
+    const uint32_t addr = smem_u32(bar);
+    auto tried = [&]() {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(addr), "r"(parity), "r"(20000u)
+                     : "memory");
+        return ok != 0u;
+    };
+    if (tried()) return true;
+    const uint64_t t0 = global_ns();
+    while (!tried())
+        if (global_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+
 // Shared-memory matrix descriptor (Blackwell format): start address, leading and
 // stride byte offsets in 16-byte units, descriptor version 1 (bits 46-47) and the
 // layout/swizzle mode in bits 61-63 (0 none, 2 = 128-byte swizzle).

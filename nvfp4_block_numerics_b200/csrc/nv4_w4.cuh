@@ -29,6 +29,7 @@
 
 #include "nv4_async.cuh"
 #include "nv4_common.cuh"
+#include "nv4_cpasync.cuh"
 
 namespace nv4 {
 namespace w4 {
@@ -41,16 +42,6 @@ constexpr int kDepth32 = 2;                       // chunks of 2 x 16 rows
 constexpr uint32_t kSlot = 16u * 128u + 16u * 16u;          // codes and scales of 16 rows x 256
 constexpr uint32_t kRing = kWarps * kDepth * kSlot;         // bytes for all warps
 constexpr uint32_t kRing32 = kWarps * kDepth32 * 2u * kSlot;
-
-// Copies n of kBytes (0 or kBytes) bytes and fills up with zeros.
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t n)
-{
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
-}
 
 // Where this lane's share of a tile's rows g (a) and g + 8 (b) lies, and the bytes a copy of it
 // has (0: no such row).  Set once per tile; chunk c is a constant offset away.

@@ -12,9 +12,12 @@
 //   * warp 0, one lane: 2-D TMA of x, kTok rows x 64 K-elements per stage (128-byte swizzle, zeros
 //     outside), a ring of kStages that runs across tiles.
 //   * warp 1: owns the tensor memory; one lane issues four MMAs (K = 16) per stage.
-//   * warps 4-11: decoders, thread = weight row (the tensor memory lane it may write), two sets of
-//     four warps that take alternate stages.  A thread loads its row's 32 bytes of codes and 4
-//     scales of the stage after next while it decodes, and writes 32 columns (tcgen05.st).
+//   * warps 4-11: decoders, two sets of four; a warp owns 32 weight rows (the tensor memory lanes
+//     it may write) and takes every other 256-element chunk of K.  It fills a ring in shared memory
+//     for itself with cp.async, eight lanes to a row's 128 bytes, across the ends of tiles; then
+//     each lane decodes the codes of one row and writes 32 columns per stage (tcgen05.st).  (With
+//     each lane loading its own row from global memory, 32 lines per instruction, the load path
+//     set the pace: 895 clocks per stage, 245 us for 4096 x 16384 x 2048.)
 //   * warps 12-19: epilogue, two warps per 32 lanes, half the columns each; 16-bit outputs leave
 //     through a 2 KB transpose per warp so that a store covers 64 bytes of an output row.
 // With few tiles a cluster of z CTAs shares one: each multiplies its part of K, the partial sums
@@ -22,6 +25,7 @@
 // Every mbarrier wait is bounded (kWaitLimitNs), as in gemm.cu.
 #include <type_traits>
 
+#include "nv4_cpasync.cuh"
 #include "nv4_internal.h"
 #include "nv4_tcgen05.cuh"
 #include "nv4_tensormap.h"
@@ -33,9 +37,12 @@ namespace w4mma {
 using namespace tc;
 
 constexpr int kThreads = 640;
-constexpr int kABufs = 4;                         // decoded stages in tensor memory, 32 columns each
+constexpr int kABufs = 8;                         // decoded stages in tensor memory, 32 columns each
 constexpr uint32_t kACol = 256;                   // behind the accumulator's columns
-constexpr int kStages = 6;
+constexpr int kDepth = 2;                         // chunks of 256 K-elements in flight per decoder warp
+constexpr uint32_t kSlot = 32u * 128u + 32u * 16u;          // codes and scales of 32 rows x 256
+template <int kTok>
+constexpr int kStages = kTok == 256 ? 4 : 6;      // stages of x
 
 struct Params {
     CUtensorMap map_x;                            // x [T, K], boxes of kTok rows x 64 elements
@@ -44,16 +51,17 @@ struct Params {
     const float* d_s2;
     void* out;
     int64_t ldd;
-    uint32_t T, N, K, z, n_tiles, tiles, stages;  // n_tiles: of 128 weight rows; stages of 64 K-elements
+    uint32_t T, N, K, z, n_tiles, tiles, chunks;  // n_tiles: of 128 weight rows; chunks of 256 K-elements
     uint32_t vec;                                 // 16-byte stores of 16-bit outputs are aligned
     uint32_t* d_flags;
 };
 
 template <int kTok>
 struct Smem {
-    uint8_t x[kStages][kTok * 128];               // 1024-byte aligned
+    uint8_t x[kStages<kTok>][kTok * 128];         // 1024-byte aligned
+    uint8_t ring[8][kDepth * kSlot];
     uint8_t stg[8][2048];
-    uint64_t full[kStages], empty[kStages], a_full[kABufs], a_free[kABufs], acc_full, acc_empty, drain;
+    uint64_t full[kStages<kTok>], empty[kStages<kTok>], a_full[kABufs], a_free[kABufs], acc_full, acc_empty, drain;
     uint32_t tmem_base, abort, issued, consumed;
 };
 
@@ -65,35 +73,6 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint64
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
                  "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
                  : "memory");
-}
-
-// 64 codes and 4 scales of a weight row from element k on; zeros past K or where not live.
-template <bool kVec>
-__device__ __forceinline__ void load64(uint32_t (&q)[8], uint32_t& s, const uint8_t* qrow, const uint8_t* srow, uint32_t k,
-                                       uint32_t K, bool live)
-{
-    s = 0u;
-    if constexpr (kVec) {
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (live && k < K) {
-            a = __ldg(reinterpret_cast<const uint4*>(qrow + (k >> 1)));
-            b = __ldg(reinterpret_cast<const uint4*>(qrow + (k >> 1) + 16u));
-            s = __ldg(reinterpret_cast<const uint32_t*>(srow + (k >> 4)));
-        }
-        q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
-        q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
-    } else {
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-            uint2 v = make_uint2(0u, 0u);
-            if (live && k + 16u * j < K) {
-                v = __ldg(reinterpret_cast<const uint2*>(qrow + (k >> 1) + 8u * j));
-                s |= (uint32_t)__ldg(srow + (k >> 4) + j) << (8u * j);
-            }
-            q[2 * j] = v.x;
-            q[2 * j + 1] = v.y;
-        }
-    }
 }
 
 // The 64 values as 32 words of two: FP16 by conversion and multiply, BF16 by converting those
@@ -152,15 +131,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
 {
     // kind::f16: FP32 accumulator (bit 4), A and B types in bits 7 and 10 (0 FP16, 1 BF16), both
     // K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28
+    constexpr int kStages = w4mma::kStages<kTok>;
     constexpr uint32_t kIdesc = (1u << 4) | (kDt == 0 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTok >> 3) << 17) |
                                 ((128u >> 4) << 24);
     extern __shared__ uint8_t smem_raw[];
     Smem<kTok>& sm = *reinterpret_cast<Smem<kTok>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<kTok>) + 15u) & ~size_t(15)));   // [kTok][128], z > 1
+    float* part = reinterpret_cast<float*>(&sm.x[0][0]);           // z > 1: [kTok][128], once the last product has read x
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = p.z > 1u ? cluster_ctarank() : 0u;
     const uint32_t clu = blockIdx.x / p.z, nclu = gridDim.x / p.z;
-    const uint32_t ks0 = rank * p.stages / p.z, KS = (rank + 1u) * p.stages / p.z - ks0;   // this CTA's stages of a tile
+    const uint32_t ch0 = rank * p.chunks / p.z, NC = (rank + 1u) * p.chunks / p.z - ch0;   // this CTA's chunks of a tile
+    const uint32_t KS = (min(p.K, (ch0 + NC) * 256u) - ch0 * 256u + 63u) / 64u;            // and stages of 64
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -194,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
                 const int tok0 = (int)((t / p.n_tiles) * kTok);
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages;
-                    if (g >= (uint32_t)kStages && !mbar_wait(&sm.empty[s], ((g / kStages) - 1u) & 1u)) give_up();
+                    if (g >= (uint32_t)kStages && !wait_bar(&sm.empty[s], ((g / kStages) - 1u) & 1u)) give_up();
                     if (aborted()) break;
                     mbar_arrive_expect_tx(&sm.full[s], kTok * 128u);
-                    tma_load_2d(sm.x[s], &p.map_x, &sm.full[s], (int)((ks0 + ks) * 64u), tok0);
+                    tma_load_2d(sm.x[s], &p.map_x, &sm.full[s], (int)(ch0 * 256u + ks * 64u), tok0);
                 }
             }
             sm.issued = g;
@@ -207,14 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         if (lane == 0) {                                           // MMA issuer
             uint32_t g = 0, i = 0;
             for (uint32_t t = clu; t < p.tiles && !aborted(); t += nclu, ++i) {
-                if (i > 0 && !mbar_wait(&sm.acc_empty, (i - 1u) & 1u)) {
+                if (i > 0 && !wait_bar(&sm.acc_empty, (i - 1u) & 1u)) {
                     give_up();
                     break;
                 }
                 tc_fence_after();
                 for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
                     const uint32_t s = g % kStages, b = g % kABufs;
-                    if (!mbar_wait(&sm.full[s], (g / kStages) & 1u) || !mbar_wait(&sm.a_full[b], (g / kABufs) & 1u)) {
+                    if (!wait_bar(&sm.full[s], (g / kStages) & 1u) || !wait_bar(&sm.a_full[b], (g / kABufs) & 1u)) {
                         give_up();
                         break;
                     }
@@ -231,56 +212,106 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
             }
             sm.consumed = g;
             tc_commit(&sm.drain);
-            if (!mbar_wait(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
-        // ---- decoders: set 0 the even, set 1 the odd stages (counted over all tiles)
-        const uint32_t quad = (uint32_t)warp & 3u, lanes = (32u * quad) << 16;
-        uint32_t t = clu, ks = 0u, g = ((uint32_t)warp - 4u) >> 2;
-        const uint8_t *qrow = nullptr, *srow = nullptr;
-        bool live = false;
-        auto settle = [&]() {                                      // (t, ks) of stage ks past the tile's end
-            while (t < p.tiles && ks >= KS) {
-                ks -= KS;
+        // ---- decoders: set 0 the even, set 1 the odd chunks (counted over all tiles)
+        const uint32_t quad = (uint32_t)warp & 3u, set = ((uint32_t)warp - 4u) >> 2, piece = (uint32_t)lane & 7u,
+                       sub = (uint32_t)lane >> 3;
+        uint8_t* ring = sm.ring[warp - 4];
+        const size_t pitch = p.K / 2u, spitch = p.K / 16u;
+        uint32_t lt = clu, lc = set, ut = clu, uc = set, base = 0u;            // (tile, chunk) to load, to decode; stages before
+        auto settle = [&](uint32_t& t, uint32_t& c) {
+            while (t < p.tiles && c >= NC) {
+                c -= NC;
                 t += nclu;
             }
         };
-        auto fetch = [&](uint32_t (&q)[8], uint32_t& s) {
-            if (t >= p.tiles) return;
-            const uint32_t row = (t % p.n_tiles) * 128u + 32u * quad + (uint32_t)lane;
-            live = row < p.N;
-            qrow = p.q + (size_t)row * (p.K / 2u);
-            srow = p.sc + (size_t)row * (p.K / 16u);
-            load64<kVec>(q, s, qrow, srow, (ks0 + ks) * 64u, p.K, live);
-        };
-        ks = g;
-        settle();
-        uint32_t q[8], s = 0u;
-        fetch(q, s);
-        bool quit = false;
-        while (t < p.tiles && !quit) {
-            uint32_t o[32];
-            decode64<kDt>(o, q, s);
-            ks += 2u;
-            settle();
-            fetch(q, s);                                           // the set's next stage, in flight from here
-            const uint32_t b = g % kABufs;
-            const bool ok = g < (uint32_t)kABufs || mbar_wait(&sm.a_free[b], ((g / kABufs) - 1u) & 1u);
-            const bool timed_out = __any_sync(0xFFFFFFFFu, !ok);
-            quit = timed_out || __any_sync(0xFFFFFFFFu, aborted());
-            if (quit) {
-                if (timed_out && lane == 0) give_up();
-                break;
+        auto load = [&](uint32_t at) {
+            if (lt < p.tiles) {
+                const uint32_t row0 = (lt % p.n_tiles) * 128u + 32u * quad, live = row0 < p.N ? min(32u, p.N - row0) : 0u;
+                const uint32_t dst = smem_u32(ring) + at * kSlot, ks = (ch0 + lc) * 256u, k = ks + 32u * piece;
+                const uint8_t* src = p.q + (size_t)(row0 + sub) * pitch + k / 2u;
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) {                 // rows sub + 4 i, 16-byte piece XOR row
+                    const uint32_t r = sub + 4u * i, d = dst + 128u * r + 16u * (piece ^ (r & 7u));
+                    if constexpr (kVec) {
+                        const bool ok = r < live && k < p.K;
+                        cp_async<16>(d, ok ? src : p.q, ok ? 16u : 0u);
+                    } else {
+#pragma unroll
+                        for (uint32_t h = 0; h < 2; ++h) {
+                            const bool ok = r < live && k + 16u * h < p.K;
+                            cp_async<8>(d + 8u * h, ok ? src + 8u * h : p.q, ok ? 8u : 0u);
+                        }
+                    }
+                    src += 4u * pitch;
+                }
+                const uint8_t* ss = p.sc + (size_t)(row0 + lane) * spitch + ks / 16u;
+                const uint32_t sd = dst + 4096u + 16u * lane;
+                const bool mine = (uint32_t)lane < live;
+                if constexpr (kVec) {
+#pragma unroll
+                    for (uint32_t h = 0; h < 4; ++h) {
+                        const bool ok = mine && ks + 64u * h < p.K;
+                        cp_async<4>(sd + 4u * h, ok ? ss + 4u * h : p.sc, ok ? 4u : 0u);
+                    }
+                } else {
+#pragma unroll
+                    for (uint32_t h = 0; h < 4; ++h) {
+                        uint32_t w = 0u;
+#pragma unroll
+                        for (uint32_t b = 0; b < 4; ++b)
+                            if (mine && ks + 64u * h + 16u * b < p.K) w |= (uint32_t)__ldg(ss + 4u * h + b) << (8u * b);
+                        *reinterpret_cast<uint32_t*>(ring + at * kSlot + 4096u + 16u * lane + 4u * h) = w;
+                    }
+                }
+                lc += 2u;
+                settle(lt, lc);
             }
-            tc_fence_after();
-            tmem_st<32>(tmem + lanes + kACol + 32u * b, o);
-            tmem_st_wait();
-            tc_fence_before();
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        settle(lt, lc);
+        settle(ut, uc);
+        base = (ut - clu) / nclu * KS;
+        for (uint32_t i = 0; i < (uint32_t)kDepth; ++i) load(i);
+        bool quit = false;
+        for (uint32_t at = 0u; ut < p.tiles && !quit; at = at + 1u == (uint32_t)kDepth ? 0u : at + 1u) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.a_full[b]);
-            g += 2u;
+            const uint8_t* slot = ring + at * kSlot;
+            const uint32_t ns = min(4u, KS - 4u * uc);
+#pragma unroll 1
+            for (uint32_t i = 0; i < ns; ++i) {
+                const uint32_t g = base + 4u * uc + i, b = g % kABufs;
+                const uint4 qa = *reinterpret_cast<const uint4*>(slot + 128u * lane + 16u * ((2u * i) ^ (lane & 7u)));
+                const uint4 qb = *reinterpret_cast<const uint4*>(slot + 128u * lane + 16u * ((2u * i + 1u) ^ (lane & 7u)));
+                const uint32_t q[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+                uint32_t o[32];
+                decode64<kDt>(o, q, *reinterpret_cast<const uint32_t*>(slot + 4096u + 16u * lane + 4u * i));
+                const bool ok = g < (uint32_t)kABufs || wait_bar(&sm.a_free[b], ((g / kABufs) - 1u) & 1u);
+                const bool timed_out = __any_sync(0xFFFFFFFFu, !ok);
+                quit = timed_out || __any_sync(0xFFFFFFFFu, aborted());
+                if (quit) {
+                    if (timed_out && lane == 0) give_up();
+                    break;
+                }
+                tc_fence_after();
+                tmem_st<32>(tmem + ((32u * quad) << 16) + kACol + 32u * b, o);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.a_full[b]);
+            }
+            __syncwarp();                                          // the slot has been read
+            if (quit) break;
+            load(at);
+            uc += 2u;
+            settle(ut, uc);
+            base = (ut - clu) / nclu * KS;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
     } else if (warp >= 12) {
         // ---- epilogue: lanes 32 quad .. + 31 (one weight row per thread), columns (tokens) of half h
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         constexpr uint32_t kCols = kTok / 2;
         uint32_t i = 0;
         for (uint32_t t = clu; t < p.tiles; t += nclu, ++i) {
-            const bool ok = !aborted() && mbar_wait(&sm.acc_full, i & 1u);
+            const bool ok = !aborted() && wait_bar(&sm.acc_full, i & 1u);
             if (!ok) {
                 if (!aborted()) give_up();
                 break;
@@ -371,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
     __syncthreads();
     if (threadIdx.x == 0)
         for (uint32_t g = sm.consumed; g < sm.issued; ++g)
-            if (!mbar_wait(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
+            if (!wait_bar(&sm.full[g % kStages], (g / kStages) & 1u)) flags |= kFlagTimeout;
     if (p.z > 1u) {
         cluster_sync();
         const uint32_t n0 = (clu % p.n_tiles) * 128u, tok0 = (clu / p.n_tiles) * kTok;
@@ -416,12 +447,13 @@ static cudaError_t run(const Params& p, cudaStream_t s)
 {
     static bool ready[64] = {};
     auto kern = linear_mma_kernel<kTok, kDt, kOut, kVec>;
-    const size_t base = sizeof(Smem<kTok>) + 1024 + 16, part = kTok <= 128 ? (size_t)kTok * 512u : 0u;
+    static_assert(kTok == 256 || kStages<kTok> * 128 >= 512, "the partial sums take the place of x");
+    constexpr size_t smem = sizeof(Smem<kTok>) + 1024;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !ready[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(base + part));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
@@ -429,7 +461,7 @@ static cudaError_t run(const Params& p, cudaStream_t s)
     const uint32_t sms = (uint32_t)num_sms();
     cfg.gridDim = dim3(p.z > 1u ? p.tiles * p.z : p.tiles < sms ? p.tiles : sms, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = base + (p.z > 1u ? part : 0u);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -470,7 +502,7 @@ cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K,
     p.N = (uint32_t)N;
     p.K = (uint32_t)K;
     p.n_tiles = (uint32_t)((N + 127) / 128);
-    p.stages = (uint32_t)((K + 63) / 64);
+    p.chunks = (uint32_t)((K + 255) / 256);
     p.vec = ldd % 8 == 0 ? 1u : 0u;
     p.d_flags = d_flags;
     const uint32_t sms = (uint32_t)num_sms();
@@ -479,11 +511,11 @@ cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K,
     auto tiles = [&](uint32_t k) { return p.n_tiles * (uint32_t)((T + k - 1) / k); };
     if (tok == 256u && tiles(256u) < sms) tok = 128u;
     p.tiles = tiles(tok);
-    // split K in clusters while there are SMs for it and every CTA keeps four stages
+    // split K in clusters while there are SMs for it and every CTA keeps a chunk
     p.z = 1u;
-    while (tok <= 128u && p.z < 8u && p.tiles * p.z * 2u <= sms && p.stages >= 8u * p.z) p.z *= 2u;
+    while (tok <= 128u && p.z < 8u && p.tiles * p.z * 2u <= sms && p.chunks >= 2u * p.z) p.z *= 2u;
     if (!x_map(&p.map_x, x, dt, T, K, ldx, tok)) return cudaErrorInvalidValue;
-    const bool vec = K % 64 == 0;                                  // (32-byte code runs, 4-byte aligned scales)
+    const bool vec = K % 64 == 0;                                  // (16-byte aligned codes, 4-byte aligned scales)
     if (tok == 32u) return pick<32>(p, dt, out_dt, vec, s);
     if (tok == 64u) return pick<64>(p, dt, out_dt, vec, s);
     if (tok == 128u) return pick<128>(p, dt, out_dt, vec, s);
