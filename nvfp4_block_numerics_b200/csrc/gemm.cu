@@ -174,46 +174,49 @@ gemm_nvfp4_kernel(const __grid_constant__ Params p)
         }
         __syncwarp();
     } else if (warp == kIssuer / 32) {
-        if (lane == 0) {                                           // MMA issuer
-            uint32_t g = 0, i = 0;
-            for (uint32_t t = blockIdx.x; t < p.tiles && !aborted(); t += gridDim.x, ++i) {
-                // the accumulator is free once the epilogue has read the previous tile
-                if (i > 0 && !wait_bar(&sm.acc_empty, (i - 1u) & 1u)) {
-                    flags |= kFlagTimeout;
-                    atomicOr(&sm.abort, 1u);
-                    break;
-                }
+        // ---- MMA issuer
+        const uint64_t da0 = smem_desc(smem_u32(sm.a[0]), 1u, 64u, 2u), db0 = smem_desc(smem_u32(sm.b[0]), 1u, 64u, 2u);
+        uint32_t g = 0, i = 0, s = 0, ph = 0;                      // kStages == kSfBufs: stage s uses buffer s
+        static_assert(kStages == kSfBufs, "stage and scale buffer advance together");
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++i) {
+            // the accumulator is free once the epilogue has read the previous tile
+            if (i > 0) ok = wait_bar_warp(&sm.acc_empty, (i - 1u) & 1u);
+            tc_fence_after();
+            for (uint32_t ks = 0; ok && ks < KS; ++ks, ++g) {
+                ok = wait_bar_warp(&sm.full[s], ph) && wait_bar_warp(&sm.sf_full[s], ph);
+                if (!ok) break;
                 tc_fence_after();
-                for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
-                    const uint32_t s = g % kStages;
-                    const uint32_t b = g % kSfBufs;
-                    if (!wait_bar(&sm.full[s], (g / kStages) & 1u) ||
-                        !wait_bar(&sm.sf_full[b], (g / kSfBufs) & 1u)) {
-                        flags |= kFlagTimeout;
-                        atomicOr(&sm.abort, 1u);
-                        break;
-                    }
-                    tc_fence_after();
-                    // scale columns (written by the scale writers): A row r of K-step j at column
-                    // ta + 4j + r/32, B row n at tb + nb*j + n/32
-                    constexpr uint32_t nb = 4u * (kBN / 128);
-                    const uint32_t ta = tmem + kBN + C::kSfCols * b, tb = ta + 16u;
-                    const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.b[s]);
+                // scale columns (written by the scale writers): A row r of K-step j at column
+                // ta + 4j + r/32, B row n at tb + nb*j + n/32
+                constexpr uint32_t nb = 4u * (kBN / 128);
+                const uint32_t ta = tmem + kBN + C::kSfCols * s, tb = ta + 16u;
+                const uint64_t da = da0 + (uint64_t)(s * (C::kATile / 16u)), db = db0 + (uint64_t)(s * (C::kBTile / 16u));
+                if (elect_one()) {
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j)
-                        mma_fp4<false, false>(tmem, smem_desc(a0 + 32u * j, 1u, 64u, 2u), smem_desc(b0 + 32u * j, 1u, 64u, 2u),
-                                C::kIdesc, ta + 4u * j, tb + nb * j, (ks | j) != 0u ? 1u : 0u);
+                        mma_fp4<false, false>(tmem, da + 2u * j, db + 2u * j, C::kIdesc, ta + 4u * j, tb + nb * j,
+                                              (ks | j) != 0u ? 1u : 0u);
                     tc_commit(&sm.empty[s]);                       // frees the stage when these MMAs finish
-                    tc_commit(&sm.sf_free[b]);                     // and the scale buffer
+                    tc_commit(&sm.sf_free[s]);                     // and the scale buffer
                 }
-                if (aborted()) break;
-                tc_commit(&sm.acc_full);                           // this tile's accumulator is complete
+                __syncwarp();
+                if (++s == (uint32_t)kStages) {
+                    s = 0u;
+                    ph ^= 1u;
+                }
             }
-            sm.consumed = g;
-            tc_commit(&sm.drain);                                  // every tensor-core operation issued
-            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (ok && elect_one()) tc_commit(&sm.acc_full);        // this tile's accumulator is complete
+            __syncwarp();
         }
+        if (!ok && lane == 0) {
+            flags |= kFlagTimeout;
+            atomicOr(&sm.abort, 1u);
+        }
+        if (lane == 0) sm.consumed = g;
+        if (elect_one()) tc_commit(&sm.drain);                     // every tensor-core operation issued
         __syncwarp();
+        if (!wait_bar_warp(&sm.drain, 0u)) flags |= kFlagTimeout;
     } else if (warp >= 4 && warp < 8) {
         // ---- scale writers, warps 4-7 (tensor-memory sub-partition q = warp % 4, lanes
         // 32q..32q+31).  The block-scaled MMA reads the scale factors of a K-step from the
@@ -466,41 +469,46 @@ gemm_pair_kernel(const __grid_constant__ Params p)
         }
         __syncwarp();
     } else if (warp == kIssuer / 32) {
-        if (lane == 0 && rank == 0) {                              // the pair's MMA issuer
-            uint32_t g = 0, i = 0;
-            for (uint32_t t = pair; t < p.tiles && !aborted(); t += npairs, ++i) {
-                if (i > 0 && !wait_bar(&sm.acc_empty, (i - 1u) & 1u)) {
-                    give_up();
-                    break;
-                }
+        if (rank == 0) {                                           // the pair's MMA issuer
+            const uint64_t da0 = smem_desc(smem_u32(sm.a[0]), 1u, 64u, 2u), db0 = smem_desc(smem_u32(sm.b[0]), 1u, 64u, 2u);
+            uint32_t g = 0, i = 0, s = 0, ph = 0;                  // kStages2 == kSfBufs2: stage s uses buffer s
+            static_assert(kStages2 == kSfBufs2, "stage and scale buffer advance together");
+            bool ok = true;
+            for (uint32_t t = pair; ok && t < p.tiles; t += npairs, ++i) {
+                if (i > 0) ok = wait_bar_warp(&sm.acc_empty, (i - 1u) & 1u);
                 tc_fence_after();
-                for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
-                    const uint32_t s = g % kStages, b = g % kSfBufs2, ph = (g / kStages) & 1u;
-                    if (!wait_bar(&sm.full[s], ph) || !wait_bar(&sm.sf_full[b], (g / kSfBufs2) & 1u) ||
-                        !wait_bar(&sm.peer_ready[s], ph)) {
-                        give_up();
-                        break;
-                    }
+                for (uint32_t ks = 0; ok && ks < KS; ++ks, ++g) {
+                    ok = wait_bar_warp(&sm.full[s], ph) && wait_bar_warp(&sm.sf_full[s], ph) &&
+                         wait_bar_warp(&sm.peer_ready[s], ph);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t ta = tmem + 256u + C::kSfCols * b, tb = ta + 16u;
-                    const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.b[s]);
+                    const uint32_t ta = tmem + 256u + C::kSfCols * s, tb = ta + 16u;
+                    const uint64_t da = da0 + (uint64_t)(s * 1024u), db = db0 + (uint64_t)(s * 1024u);
+                    if (elect_one()) {
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) {
-                        // MXFP4: an atom's words serve two steps, the second from byte 2 on
-                        const uint32_t at = kMx ? j >> 1 : j, id = kMx ? 2u * (j & 1u) : 0u;
-                        mma_fp4<true, kMx>(tmem, smem_desc(a0 + 32u * j, 1u, 64u, 2u),
-                                           smem_desc(b0 + 32u * j, 1u, 64u, 2u), kIdesc2 | (id << 29) | (id << 4),
-                                           ta + 4u * at, tb + 8u * at, (ks | j) != 0u ? 1u : 0u);
+                        for (uint32_t j = 0; j < 4; ++j) {
+                            // MXFP4: an atom's words serve two steps, the second from byte 2 on
+                            const uint32_t at = kMx ? j >> 1 : j, id = kMx ? 2u * (j & 1u) : 0u;
+                            mma_fp4<true, kMx>(tmem, da + 2u * j, db + 2u * j, kIdesc2 | (id << 29) | (id << 4), ta + 4u * at,
+                                               tb + 8u * at, (ks | j) != 0u ? 1u : 0u);
+                        }
+                        tc_commit_pair(&sm.empty[s]);
+                        tc_commit_pair(&sm.sf_free[s]);
                     }
-                    tc_commit_pair(&sm.empty[s]);
-                    tc_commit_pair(&sm.sf_free[b]);
+                    __syncwarp();
+                    if (++s == (uint32_t)kStages) {
+                        s = 0u;
+                        ph ^= 1u;
+                    }
                 }
-                if (aborted()) break;
-                tc_commit_pair(&sm.acc_full);
+                if (ok && elect_one()) tc_commit_pair(&sm.acc_full);
+                __syncwarp();
             }
-            sm.consumed = g;
-            tc_commit_pair(&sm.drain);
-            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (!ok && lane == 0) give_up();
+            if (lane == 0) sm.consumed = g;
+            if (elect_one()) tc_commit_pair(&sm.drain);
+            __syncwarp();
+            if (!wait_bar_warp(&sm.drain, 0u)) flags |= kFlagTimeout;
         } else if (lane == 0) {                                    // rank 1: forwards its landed stages
             uint32_t g = 0;
             for (uint32_t t = pair; t < p.tiles && !aborted(); t += npairs) {

@@ -125,32 +125,37 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t ks = 0;
-            for (; ks < KS; ++ks) {
-                const uint32_t s = ks % kStages, b = ks % kSfBufs;
-                if (!wait_bar(&sm.full[s], (ks / kStages) & 1u) || !wait_bar(&sm.sf_full[b], (ks / kSfBufs) & 1u)) {
-                    give_up();
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t w0 = smem_u32(sm.w[s]), x0 = smem_u32(sm.x[s]), f0 = tmem + kSfCol + 16u * b;
+        // ---- MMA issuer
+        const uint64_t dw0 = smem_desc(smem_u32(sm.w[0]), 1u, 64u, 2u), dx0 = smem_desc(smem_u32(sm.x[0]), 1u, 64u, 2u);
+        uint32_t ks = 0;
+        bool ok = true;
+        for (; ks < KS; ++ks) {
+            const uint32_t s = ks % kStages, b = ks % kSfBufs;
+            ok = wait_bar_warp(&sm.full[s], (ks / kStages) & 1u) && wait_bar_warp(&sm.sf_full[b], (ks / kSfBufs) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dw = dw0 + (uint64_t)(s * 1024u), dx = dx0 + (uint64_t)(s * (kTok * 8u));
+            const uint32_t f0 = tmem + kSfCol + 16u * b;
+            if (elect_one()) {
 #pragma unroll
                 for (uint32_t j = 0; j < 4; ++j) {
                     const uint32_t id = 2u * (j & 1u);
-                    mma_fp4<false, true>(tmem, smem_desc(w0 + 32u * j, 1u, 64u, 2u), smem_desc(x0 + 32u * j, 1u, 64u, 2u),
-                                         kIdesc | (id << 29) | (id << 4), f0 + 4u * (j >> 1), f0 + 8u + 4u * (j >> 1),
-                                         (ks | j) != 0u ? 1u : 0u);
+                    mma_fp4<false, true>(tmem, dw + 2u * j, dx + 2u * j, kIdesc | (id << 29) | (id << 4), f0 + 4u * (j >> 1),
+                                         f0 + 8u + 4u * (j >> 1), (ks | j) != 0u ? 1u : 0u);
                 }
                 tc_commit(&sm.empty[s]);
                 tc_commit(&sm.sf_free[b]);
             }
-            sm.consumed = ks;
-            if (ks == KS) tc_commit(&sm.acc_full);
+            __syncwarp();
+        }
+        if (!ok && lane == 0) give_up();
+        if (lane == 0) sm.consumed = ks;
+        if (elect_one()) {
+            if (ok) tc_commit(&sm.acc_full);
             tc_commit(&sm.drain);
-            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
         }
         __syncwarp();
+        if (!wait_bar_warp(&sm.drain, 0u)) flags |= kFlagTimeout;
     } else if (warp >= 4) {
         const uint32_t quad = (uint32_t)warp & 3u, lanes = (32u * quad) << 16;
         bool quit = false;

@@ -29,6 +29,23 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity)
     return true;
 }
 
+// Every lane of a warp waits; whether all of them saw the phase.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity)
+{
+    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity)) != 0;
+}
+
+// One lane of the warp.  The issuing warps walk their stages with all lanes and issue under this:
+// addresses and descriptors are then the same for the whole warp, as the instructions want them.
+// (With the loop itself under a lane test the four MMAs and two commits of a stage took 550 clocks
+// to issue, whatever their size.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0u;
+}
+
 // Shared-memory matrix descriptor (Blackwell format): start address, leading and
 // stride byte offsets in 16-byte units, descriptor version 1 (bits 46-47) and the
 // layout/swizzle mode in bits 61-63 (0 none, 2 = 128-byte swizzle).

@@ -185,36 +185,43 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {                                           // MMA issuer
-            uint32_t g = 0, i = 0;
-            for (uint32_t t = clu; t < p.tiles && !aborted(); t += nclu, ++i) {
-                if (i > 0 && !wait_bar(&sm.acc_empty, (i - 1u) & 1u)) {
-                    give_up();
-                    break;
-                }
+        // ---- MMA issuer
+        const uint64_t desc0 = smem_desc(smem_u32(sm.x[0]), 1u, 64u, 2u);
+        uint32_t g = 0u, i = 0u, s = 0u, b = 0u, sp = 0u, bp = 0u;    // stage and buffer, their phases
+        bool ok = true;
+        for (uint32_t t = clu; ok && t < p.tiles; t += nclu, ++i) {
+            if (i > 0u) ok = wait_bar_warp(&sm.acc_empty, (i - 1u) & 1u);
+            tc_fence_after();
+            for (uint32_t ks = 0; ok && ks < KS; ++ks, ++g) {
+                ok = wait_bar_warp(&sm.full[s], sp) && wait_bar_warp(&sm.a_full[b], bp);
+                if (!ok) break;
                 tc_fence_after();
-                for (uint32_t ks = 0; ks < KS; ++ks, ++g) {
-                    const uint32_t s = g % kStages, b = g % kABufs;
-                    if (!wait_bar(&sm.full[s], (g / kStages) & 1u) || !wait_bar(&sm.a_full[b], (g / kABufs) & 1u)) {
-                        give_up();
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t x0 = smem_u32(sm.x[s]), a0 = tmem + kACol + 32u * b;
+                const uint64_t desc = desc0 + (uint64_t)(s * (kTok * 8u));
+                const uint32_t a0 = tmem + kACol + 32u * b;
+                if (elect_one()) {
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j)
-                        mma_f16(tmem, a0 + 8u * j, smem_desc(x0 + 32u * j, 1u, 64u, 2u), kIdesc, (ks | j) != 0u ? 1u : 0u);
+                    for (uint32_t j = 0; j < 4; ++j) mma_f16(tmem, a0 + 8u * j, desc + 2u * j, kIdesc, (ks | j) != 0u ? 1u : 0u);
                     tc_commit(&sm.empty[s]);
                     tc_commit(&sm.a_free[b]);
                 }
-                if (aborted()) break;
-                tc_commit(&sm.acc_full);
+                __syncwarp();
+                if (++s == (uint32_t)kStages) {
+                    s = 0u;
+                    sp ^= 1u;
+                }
+                if (++b == (uint32_t)kABufs) {
+                    b = 0u;
+                    bp ^= 1u;
+                }
             }
-            sm.consumed = g;
-            tc_commit(&sm.drain);
-            if (!wait_bar(&sm.drain, 0u)) flags |= kFlagTimeout;
+            if (ok && elect_one()) tc_commit(&sm.acc_full);
+            __syncwarp();
         }
+        if (!ok && lane == 0) give_up();
+        if (lane == 0) sm.consumed = g;
+        if (elect_one()) tc_commit(&sm.drain);
         __syncwarp();
+        if (!wait_bar_warp(&sm.drain, 0u)) flags |= kFlagTimeout;
     } else if (warp >= 4 && warp < 12) {
         // ---- decoders: set 0 the even, set 1 the odd chunks (counted over all tiles)
         const uint32_t quad = (uint32_t)warp & 3u, set = ((uint32_t)warp - 4u) >> 2, piece = (uint32_t)lane & 7u,
