@@ -11,6 +11,7 @@ their outputs with torch and call the same entry points.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import threading
 
@@ -751,13 +752,13 @@ def _new(shape, dtype, x: torch.Tensor, stream) -> torch.Tensor:
 
 
 def _bytes(t: torch.Tensor, shape, name: str) -> int:
-    if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous():
         raise NV4Error(f"{name} must be a contiguous uint8 tensor {tuple(shape)}")
     return t.data_ptr()
 
 
 def _f32_n(t: torch.Tensor, n: int, name: str):
-    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
         raise NV4Error(f"{name} must be a contiguous float32 tensor of {n}")
     return t.data_ptr()
 
@@ -829,6 +830,7 @@ def _moe_shapes(x, gate, down, out, work, k: int):
     return T, H, ldx, E, I, max(ldd, H) if T <= 1 else ldd
 
 
+@functools.lru_cache(maxsize=4096)
 def nv4_moe_work_bytes(T: int, top_k: int, H: int, I: int) -> int:
     return int(lib().nv4_moe_work_bytes(T, top_k, H, I))
 
@@ -888,15 +890,16 @@ def moe_experts(x, ids, weights, gate, up, down, dtype=None, d_flags=None, strea
 
 def moe_layer(x, w_router, gate, up, down, top_k: int, renormalize=True, dtype=None, d_flags=None, stream=None):
     """The whole layer: x [T, H] -> (out [T, H], ids, weights)."""
-    T = x.shape[0]
-    out = _new(tuple(x.shape), dtype or x.dtype, x, stream)
-    ids = _new((T, top_k), torch.int32, x, stream)
-    weights = _new((T, top_k), torch.float32, x, stream)
-    work = _new((nv4_moe_work_bytes(T, top_k, x.shape[1], gate[0].shape[1]),), torch.uint8, x, stream)
+    T, H = x.shape
+    out = _new((T, H), dtype or x.dtype, x, stream)
+    routing = _new((2, T, top_k), torch.int32, x, stream)
+    ids, weights = routing[0], routing[1].view(torch.float32)
+    work = _new((nv4_moe_work_bytes(T, top_k, H, gate[0].shape[1]),), torch.uint8, x, stream)
     nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize, d_flags, stream)
     return out, ids, weights
 
 
+@functools.lru_cache(maxsize=4096)
 def nv4_mxfp4_mma_scale_bytes(rows: int, cols: int) -> int:
     return int(lib().nv4_mxfp4_mma_scale_bytes(rows, cols))
 
@@ -953,6 +956,7 @@ def gemm_mxfp4(qa, sfa_mma, qb, sfb_mma, dtype=torch.bfloat16, d_flags=None, str
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def nv4_linear_mxfp4_work_bytes(M: int, K: int) -> int:
     return int(lib().nv4_linear_mxfp4_work_bytes(M, K))
 

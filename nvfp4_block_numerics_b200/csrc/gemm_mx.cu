@@ -96,19 +96,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
     if (warp == 0) {
         if (lane == 0) {
             auto weights = [&](uint32_t ks) {
-                const uint32_t s = ks % kStages, a0 = 2u * (ks0 + ks), a1 = min(a0 + 1u, p.kt - 1u);
+                const uint32_t s = ks % kStages, a0 = 2u * (ks0 + ks);
                 const uint8_t* f = p.sfw + (size_t)n_tile * p.kt * 512u;
                 mbar_arrive_expect_tx(&sm.full[s], kTx);
                 tma_load_2d(sm.w[s], &p.map_w, &sm.full[s], (int)((ks0 + ks) * 128u), (int)(n_tile * 128u));
-                bulk_load(sm.sfw[s], f + (size_t)a0 * 512u, 512u, &sm.full[s]);
-                bulk_load(sm.sfw[s] + 512u, f + (size_t)a1 * 512u, 512u, &sm.full[s]);   // past an odd end: codes are zeros
+                load_atoms(sm.sfw[s], f, a0, p.kt, &sm.full[s]);
             };
             auto rows = [&](uint32_t ks) {
-                const uint32_t s = ks % kStages, a0 = 2u * (ks0 + ks), a1 = min(a0 + 1u, p.kt - 1u);
+                const uint32_t s = ks % kStages, a0 = 2u * (ks0 + ks);
                 const uint8_t* f = p.sfx + (size_t)(m0 / 128u) * p.kt * 512u;
                 tma_load_2d(sm.x[s], &p.map_x, &sm.full[s], (int)((ks0 + ks) * 128u), (int)m0);
-                bulk_load(sm.sfx[s], f + (size_t)a0 * 512u, 512u, &sm.full[s]);
-                bulk_load(sm.sfx[s] + 512u, f + (size_t)a1 * 512u, 512u, &sm.full[s]);
+                load_atoms(sm.sfx[s], f, a0, p.kt, &sm.full[s]);
             };
             const uint32_t first = min(KS, (uint32_t)kStages);
             for (uint32_t ks = 0; ks < first; ++ks) weights(ks);

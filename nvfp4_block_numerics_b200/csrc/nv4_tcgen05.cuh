@@ -35,6 +35,21 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity)
     return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity)) != 0;
 }
 
+// Every lane of a warp waits for n barriers (bar[i], parity[i]); all are tried at once before any is
+// waited for: a try takes some 130 clocks to answer.
+template <int kN>
+__device__ __forceinline__ bool wait_bars_warp(uint64_t* const (&bar)[kN], const uint32_t (&parity)[kN], uint32_t n)
+{
+    bool seen[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) seen[i] = (uint32_t)i >= n || mbar_try_wait(bar[i], parity[i]);
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (!seen[i]) ok = ok && wait_bar(bar[i], parity[i]);
+    return __all_sync(0xFFFFFFFFu, ok) != 0;
+}
+
 // One lane of the warp.  The issuing warps walk their stages with all lanes and issue under this:
 // addresses and descriptors are then the same for the whole warp, as the instructions want them.
 // (With the loop itself under a lane test the four MMAs and two commits of a stage took 550 clocks
@@ -57,6 +72,19 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// MXFP4 scale atoms a0 and a0 + 1 (128 K-elements each) of a row tile that has kt of them; past an
+// odd end the last one again (the codes are zeros there).
+__device__ __forceinline__ void load_atoms(uint8_t* dst, const uint8_t* atoms, uint32_t a0, uint32_t kt, uint64_t* bar)
+{
+    const uint8_t* src = atoms + (size_t)a0 * 512u;
+    if (a0 + 1u < kt) {
+        bulk_load(dst, src, 1024u, bar);
+    } else {
+        bulk_load(dst, src, 512u, bar);
+        bulk_load(dst + 512u, src, 512u, bar);
+    }
+}
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols)
 {

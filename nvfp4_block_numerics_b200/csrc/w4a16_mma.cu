@@ -186,33 +186,39 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA issuer
+        // two stages at a time, so that their four barriers are tried together (kStages and kABufs are
+        // even, but a tile may end on an odd stage: the positions are counted over all tiles)
         const uint64_t desc0 = smem_desc(smem_u32(sm.x[0]), 1u, 64u, 2u);
-        uint32_t g = 0u, i = 0u, s = 0u, b = 0u, sp = 0u, bp = 0u;    // stage and buffer, their phases
+        uint32_t g = 0u, i = 0u;
         bool ok = true;
         for (uint32_t t = clu; ok && t < p.tiles; t += nclu, ++i) {
             if (i > 0u) ok = wait_bar_warp(&sm.acc_empty, (i - 1u) & 1u);
             tc_fence_after();
-            for (uint32_t ks = 0; ok && ks < KS; ++ks, ++g) {
-                ok = wait_bar_warp(&sm.full[s], sp) && wait_bar_warp(&sm.a_full[b], bp);
+            for (uint32_t ks = 0; ok && ks < KS;) {
+                const uint32_t n = min(2u, KS - ks), g1 = g + 1u;
+                uint64_t* const bar[4] = {&sm.full[g % kStages], &sm.a_full[g % kABufs], &sm.full[g1 % kStages],
+                                          &sm.a_full[g1 % kABufs]};
+                const uint32_t parity[4] = {(g / kStages) & 1u, (g / kABufs) & 1u, (g1 / kStages) & 1u, (g1 / kABufs) & 1u};
+                ok = wait_bars_warp(bar, parity, 2u * n);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t desc = desc0 + (uint64_t)(s * (kTok * 8u));
-                const uint32_t a0 = tmem + kACol + 32u * b;
-                if (elect_one()) {
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) mma_f16(tmem, a0 + 8u * j, desc + 2u * j, kIdesc, (ks | j) != 0u ? 1u : 0u);
-                    tc_commit(&sm.empty[s]);
-                    tc_commit(&sm.a_free[b]);
+                for (uint32_t u = 0; u < 2; ++u) {
+                    if (u == n) break;
+                    const uint32_t s = (g + u) % kStages, b = (g + u) % kABufs;
+                    const uint64_t desc = desc0 + (uint64_t)(s * (kTok * 8u));
+                    const uint32_t a0 = tmem + kACol + 32u * b;
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t j = 0; j < 4; ++j)
+                            mma_f16(tmem, a0 + 8u * j, desc + 2u * j, kIdesc, (ks | u | j) != 0u ? 1u : 0u);
+                        tc_commit(&sm.empty[s]);
+                        tc_commit(&sm.a_free[b]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (++s == (uint32_t)kStages) {
-                    s = 0u;
-                    sp ^= 1u;
-                }
-                if (++b == (uint32_t)kABufs) {
-                    b = 0u;
-                    bp ^= 1u;
-                }
+                ks += n;
+                g += n;
             }
             if (ok && elect_one()) tc_commit(&sm.acc_full);
             __syncwarp();
