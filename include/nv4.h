@@ -481,9 +481,9 @@ NV4_API nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, con
 
 /* nv4_linear_mxfp4 -- the W4A4 linear layer: nv4_mxfp4_quant_mma of x [M, K] (dt NV4_BF16 or
  * NV4_FP32), then nv4_gemm_mxfp4 with the weights qw, sfw_mma [N, K].  The rules of both apply.
- * d_work: nv4_linear_mxfp4_work_bytes(M, K) bytes, 16-byte aligned, not shared by calls that may
- * run at the same time; nothing has to be in it and nothing is kept in it (NV4_ERR_LIMIT if
- * work_bytes is less). */
+ * d_work: nv4_linear_mxfp4_work_bytes(M, K) bytes (0 up to 16 rows, which are quantized within the
+ * product: d_work may be NULL then), 16-byte aligned, not shared by calls that may run at the same
+ * time; nothing has to be in it and nothing is kept in it (NV4_ERR_LIMIT if work_bytes is less). */
 NV4_API size_t nv4_linear_mxfp4_work_bytes(int64_t M, int64_t K);
 NV4_API nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, int64_t ldx,
                             const uint8_t* qw, const uint8_t* sfw_mma, int64_t N, nv4_dtype out_dt, void* out,

@@ -961,9 +961,9 @@ def nv4_linear_mxfp4_work_bytes(M: int, K: int) -> int:
     return int(lib().nv4_linear_mxfp4_work_bytes(M, K))
 
 
-def nv4_linear_mxfp4(x, qw, sfw_mma, out, work, d_flags=None, stream=None):
+def nv4_linear_mxfp4(x, qw, sfw_mma, out, work=None, d_flags=None, stream=None):
     """out[M, N] = Q(x) @ W^T: x [M, K] (bf16 or float32) quantized to MXFP4, MXFP4 weights (codes
-    [N, K/2], scales in the MMA layout); work: nv4_linear_mxfp4_work_bytes(M, K) bytes."""
+    [N, K/2], scales in the MMA layout); work: nv4_linear_mxfp4_work_bytes(M, K) bytes (None if 0)."""
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise NV4Error("x must be bf16 or float32")
     dev = _here(x, qw, sfw_mma, out, work, d_flags)
@@ -974,13 +974,14 @@ def nv4_linear_mxfp4(x, qw, sfw_mma, out, work, d_flags=None, stream=None):
     orows, ocols, ldd = _rowmajor(out, "out")
     if orows != M or ocols != N:
         raise NV4Error("out must be [M, N]")
-    if not work.is_contiguous():
+    if work is not None and not work.is_contiguous():
         raise NV4Error("work must be contiguous")
     _mma_bytes(sfw_mma, N, K, "sfw_mma")
     _check(lib().nv4_linear_mxfp4(x.data_ptr(), _DT[x.dtype], M, K, max(ldx, K) if M <= 1 else ldx,
                                   _bytes(qw, (N, K // 2), "qw"), sfw_mma.data_ptr(), N, _DT[out.dtype], out.data_ptr(),
-                                  max(ldd, N) if M <= 1 else ldd, work.data_ptr(), work.numel() * work.element_size(),
-                                  _ptr(d_flags), _on(stream, dev)), "nv4_linear_mxfp4")
+                                  max(ldd, N) if M <= 1 else ldd, None if work is None else work.data_ptr(),
+                                  0 if work is None else work.numel() * work.element_size(), _ptr(d_flags),
+                                  _on(stream, dev)), "nv4_linear_mxfp4")
 
 
 def linear_mxfp4(x, qw, sfw_mma, dtype=torch.bfloat16, d_flags=None, stream=None):
@@ -988,6 +989,7 @@ def linear_mxfp4(x, qw, sfw_mma, dtype=torch.bfloat16, d_flags=None, stream=None
     in the MMA layout) -> [M, N]."""
     M, K = x.shape
     out = _new((M, qw.shape[0]), dtype, x, stream)
-    work = _new((nv4_linear_mxfp4_work_bytes(M, K),), torch.uint8, x, stream)
+    n = nv4_linear_mxfp4_work_bytes(M, K)
+    work = _new((n,), torch.uint8, x, stream) if n else None
     nv4_linear_mxfp4(x, qw, sfw_mma, out, work, d_flags, stream)
     return out

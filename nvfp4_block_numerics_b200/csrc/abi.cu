@@ -561,6 +561,7 @@ nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8
 
 size_t nv4_linear_mxfp4_work_bytes(int64_t M, int64_t K)
 {
+    if (M <= kMaxFusedRows) return 0;
     const size_t sf = nv4_mxfp4_mma_scale_bytes(M, K);             // 0 for sizes that are refused
     return sf == 0 ? 0 : sf + (size_t)M * (size_t)(K / 2);
 }
@@ -569,16 +570,27 @@ nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, i
                             const uint8_t* sfw_mma, int64_t N, nv4_dtype out_dt, void* out, int64_t ldd, void* d_work,
                             size_t work_bytes, uint32_t* d_flags, void* stream)
 {
-    uint8_t* sf = static_cast<uint8_t*>(d_work);                   // a multiple of 512 bytes
-    uint8_t* q = sf == nullptr ? nullptr : sf + nv4_mxfp4_mma_scale_bytes(M, K);
-    if (M > 0 && N > 0 && K > 0 && K % 32 == 0 && d_work != nullptr && work_bytes < nv4_linear_mxfp4_work_bytes(M, K))
-        return NV4_ERR_LIMIT;
-    nv4_status st = check_gemm_mxfp4(q, sf, qw, sfw_mma, M, N, K, out_dt, out, ldd);
+    if (dt != NV4_BF16 && dt != NV4_FP32) return NV4_ERR_DTYPE;
+    if (M > kMaxFusedRows) {
+        uint8_t* sf = static_cast<uint8_t*>(d_work);               // a multiple of 512 bytes
+        uint8_t* q = sf == nullptr ? nullptr : sf + nv4_mxfp4_mma_scale_bytes(M, K);
+        if (N > 0 && K > 0 && K % 32 == 0 && d_work != nullptr && work_bytes < nv4_linear_mxfp4_work_bytes(M, K))
+            return NV4_ERR_LIMIT;
+        nv4_status st = check_gemm_mxfp4(q, sf, qw, sfw_mma, M, N, K, out_dt, out, ldd);
+        if (st != NV4_OK || N == 0) return st;
+        st = nv4_mxfp4_quant_mma(x, dt, M, K, ldx, q, sf, d_flags, stream);
+        if (st != NV4_OK) return st;
+        return from_cuda(launch_gemm_mxfp4(q, sf, qw, sfw_mma, M, N, K, (int)out_dt, out, ldd, true, d_flags,
+                                           (cudaStream_t)stream));
+    }
+    // x stands for the quantized rows in the checks: both have to be there and 16-byte aligned
+    const uint8_t* xb = static_cast<const uint8_t*>(x);
+    const nv4_status st = check_gemm_mxfp4(xb, xb, qw, sfw_mma, M, N, K, out_dt, out, ldd);
     if (st != NV4_OK || M == 0 || N == 0) return st;
-    st = nv4_mxfp4_quant_mma(x, dt, M, K, ldx, q, sf, d_flags, stream);
-    if (st != NV4_OK) return st;
-    return from_cuda(launch_gemm_mxfp4(q, sf, qw, sfw_mma, M, N, K, (int)out_dt, out, ldd, true, d_flags,
-                                       (cudaStream_t)stream));
+    if (ldx < K) return NV4_ERR_SHAPE;
+    if (ldx % (dt == NV4_BF16 ? 8 : 4) != 0) return NV4_ERR_ALIGN;
+    return from_cuda(launch_linear_mxfp4_small(x, dt == NV4_BF16 ? 0 : 2, M, K, ldx, qw, sfw_mma, N, (int)out_dt, out, ldd,
+                                               d_flags, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------------------ products on FP4 weights

@@ -12,10 +12,14 @@
 //   * warp 1: owns the tensor memory; one lane issues four MMAs (K = 64) per stage.
 //   * warps 4-7: move the scales into tensor memory (tcgen05.st, see gemm.cu), then read the
 //     accumulator, one weight row per thread.
+//   * warps 8-11, where x comes unquantized (the linear layer, up to 16 rows): quantize their CTA's
+//     part of x into the stage, codes in the swizzled layout and scales as atoms, one stage ahead.
+//     One launch instead of two, and no workspace.
 // Every mbarrier wait is bounded (kWaitLimitNs), as in gemm.cu.
 #include <type_traits>
 
 #include "nv4_internal.h"
+#include "nv4_mxfp4.cuh"
 #include "nv4_tcgen05.cuh"
 #include "nv4_tensormap.h"
 
@@ -25,7 +29,7 @@ namespace gemmx {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                     // + 128 that quantize
 constexpr int kStages = 6;
 constexpr int kSfBufs = 4;                        // 16 columns each: 8 of the weights, 8 of the rows
 constexpr uint32_t kSfCol = 128;                  // behind the accumulator
@@ -37,7 +41,9 @@ struct Params {
     const uint8_t* sfx;
     void* out;
     int64_t ldd;
-    uint32_t M, N, z, n_tiles, stages, kt;        // kt: scale atoms per row tile
+    uint32_t M, N, K, z, n_tiles, stages, kt;     // kt: scale atoms per row tile
+    const void* x;                                // kIn >= 0: A as it came
+    int64_t ldx;
     uint32_t* d_flags;
 };
 
@@ -54,13 +60,15 @@ struct Smem {
     uint32_t tmem_base, abort, issued, consumed;
 };
 
-template <int kTok, int kOut>
-__global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid_constant__ Params p)
+// kIn: -1 A quantized, else the type of x (0 BF16, 2 FP32).
+template <int kTok, int kOut, int kIn>
+__global__ void __launch_bounds__(kIn >= 0 ? kThreads + 128 : kThreads, 1) gemm_mx_small_kernel(const __grid_constant__ Params p)
 {
     // kind::mxf4: A and B E2M1, K-major, E8M0 scales (bit 23), N >> 3 in bits 17-22, M >> 4 in bits
     // 24-28; the two bytes of a scale word that a step uses in bits 4-5 (B) and 29-30 (A)
     constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kTok >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
-    constexpr uint32_t kTx = 128u * 128u + kTok * 128u + 2048u;
+    constexpr uint32_t kTx = 128u * 128u + 1024u + (kIn >= 0 ? 0u : kTok * 128u + 1024u);
+    constexpr uint32_t kBlock = kIn >= 0 ? kThreads + 128 : kThreads;
     extern __shared__ uint8_t smem_raw[];
     Smem<kTok>& sm = *reinterpret_cast<Smem<kTok>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -70,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.full[s], kIn >= 0 ? 1 + 4 : 1);          // the copies, the quantizing warps
             mbar_init(&sm.empty[s], 1);
         }
         for (int b = 0; b < kSfBufs; ++b) {
@@ -82,7 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
         sm.abort = sm.issued = sm.consumed = 0u;
         mbar_init_fence();
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map_w)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map_x)) : "memory");
+        if constexpr (kIn < 0)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map_x)) : "memory");
     }
     if (warp == 1) tmem_alloc(&sm.tmem_base, kTmemCols);
     tc_fence_before();
@@ -103,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
                 load_atoms(sm.sfw[s], f, a0, p.kt, &sm.full[s]);
             };
             auto rows = [&](uint32_t ks) {
+                if constexpr (kIn >= 0) return;                    // the quantizing warps'
                 const uint32_t s = ks % kStages, a0 = 2u * (ks0 + ks);
                 const uint8_t* f = p.sfx + (size_t)(m0 / 128u) * p.kt * 512u;
                 tma_load_2d(sm.x[s], &p.map_x, &sm.full[s], (int)((ks0 + ks) * 128u), (int)m0);
@@ -110,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
             };
             const uint32_t first = min(KS, (uint32_t)kStages);
             for (uint32_t ks = 0; ks < first; ++ks) weights(ks);
-            asm volatile("griddepcontrol.wait;" ::: "memory");     // A is complete
+            if constexpr (kIn < 0) asm volatile("griddepcontrol.wait;" ::: "memory");     // A is complete
             for (uint32_t ks = 0; ks < first; ++ks) rows(ks);
             uint32_t ks = first;
             for (; ks < KS; ++ks) {
@@ -154,6 +164,53 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
         }
         __syncwarp();
         if (!wait_bar_warp(&sm.drain, 0u)) flags |= kFlagTimeout;
+    } else if (kIn >= 0 && warp >= 8) {
+        // ---- x of one stage: M rows x 16 half blocks, two lanes to a block
+        if constexpr (kIn >= 0) {
+            const uint32_t tid = threadIdx.x - kThreads;
+            const uint32_t kb = ks0 * 256u;
+            constexpr uint32_t kPer = kTok * 16u / 128u;           // half blocks per thread
+            float v[kPer][16];
+            uint32_t ab[kPer];
+            auto fetch = [&](uint32_t ks) {
+#pragma unroll
+                for (uint32_t j = 0; j < kPer; ++j) {
+                    const uint32_t i = tid + 128u * j, r = i >> 4, k = kb + 256u * ks + 16u * (i & 15u);
+                    ab[j] = 0u;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[j][e] = 0.0f;
+                    if (r < p.M - m0 && k < p.K && ks < KS) load16<kIn>(p.x, (int64_t)(m0 + r) * p.ldx + k, v[j], ab[j]);
+                }
+            };
+            fetch(0u);
+            for (uint32_t ks = 0; ks < KS; ++ks) {
+                const uint32_t s = ks % kStages;
+                uint32_t code[kPer], c0[kPer], c1[kPer];
+#pragma unroll
+                for (uint32_t j = 0; j < kPer; ++j) {
+                    ab[j] = max(ab[j], __shfl_xor_sync(0xFFFFFFFFu, ab[j], 1));
+                    code[j] = mxfp4_encode16(v[j], ab[j], c0[j], c1[j]);
+                    if (code[j] == 0xFFu) flags |= kFlagNonFinite;
+                }
+                fetch(ks + 1u);
+                const bool ok = ks < (uint32_t)kStages || wait_bar(&sm.empty[s], ((ks / kStages) - 1u) & 1u);
+                if (!__all_sync(0xFFFFFFFFu, ok) || __any_sync(0xFFFFFFFFu, aborted())) {
+                    if (!ok && lane == 0) give_up();
+                    break;
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < kPer; ++j) {
+                    const uint32_t i = tid + 128u * j, r = i >> 4, h = i & 15u;        // half block h of row r: block h / 2
+                    *reinterpret_cast<uint2*>(sm.x[s] + 128u * r + 16u * ((h >> 1) ^ (r & 7u)) + 8u * (h & 1u)) =
+                        make_uint2(c0[j], c1[j]);
+                    if ((h & 1u) == 0u) sm.sfx[s][512u * (h >> 3) + 16u * r + ((h >> 1) & 3u)] = (uint8_t)code[j];
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.full[s]);
+            }
+            __syncwarp();
+        }
     } else if (warp >= 4) {
         const uint32_t quad = (uint32_t)warp & 3u, lanes = (32u * quad) << 16;
         bool quit = false;
@@ -211,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
     if (!aborted()) {
         const uint32_t n0 = n_tile * 128u, rows = min(128u, p.N - n0), toks = min((uint32_t)kTok, p.M - m0);
         const uint32_t j1 = (rank + 1u) * toks * 128u / p.z;
-        for (uint32_t i = rank * toks * 128u / p.z + threadIdx.x; i < j1; i += kThreads) {
+        for (uint32_t i = rank * toks * 128u / p.z + threadIdx.x; i < j1; i += kBlock) {
             const uint32_t r = i & 127u, tok = i >> 7;
             if (r >= rows) continue;
             float sum = 0.0f;
@@ -243,11 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx_small_kernel(const __grid
     if (lane == 0) flag_or(p.d_flags, flags);
 }
 
-template <int kTok, int kOut>
+template <int kTok, int kOut, int kIn = -1>
 static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStream_t s)
 {
     static bool ready[64] = {};
-    auto kern = gemm_mx_small_kernel<kTok, kOut>;
+    auto kern = gemm_mx_small_kernel<kTok, kOut, kIn>;
     const size_t smem = sizeof(Smem<kTok>) + 1024;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -259,7 +316,7 @@ static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStre
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.z, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(kIn >= 0 ? kThreads + 128 : kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -281,6 +338,27 @@ static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStre
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+static bool fill(Params& p, const uint8_t* qw, const uint8_t* sfw, int64_t M, int64_t N, int64_t K, void* out, int64_t ldd,
+                 uint32_t tok, uint32_t* d_flags)
+{
+    if (!code_map(&p.map_w, qw, N, K, 128u)) return false;
+    p.sfw = sfw;
+    p.out = out;
+    p.ldd = ldd;
+    p.M = (uint32_t)M;
+    p.N = (uint32_t)N;
+    p.K = (uint32_t)K;
+    p.n_tiles = (uint32_t)((N + 127) / 128);
+    p.stages = (uint32_t)((K + 255) / 256);
+    p.kt = (uint32_t)((K + 127) / 128);
+    p.d_flags = d_flags;
+    // split K in clusters while there are SMs for it and every CTA keeps two stages
+    const uint32_t tiles = p.n_tiles * (uint32_t)((M + tok - 1) / tok);
+    p.z = 1u;
+    while (p.z < 8u && tiles * p.z * 2u <= (uint32_t)num_sms() && p.stages >= 4u * p.z) p.z *= 2u;
+    return true;
+}
+
 }  // namespace gemmx
 
 cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
@@ -290,20 +368,9 @@ cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const
     using namespace gemmx;
     Params p = {};
     const uint32_t tok = M <= 16 ? 16u : M <= 32 ? 32u : M <= 64 ? 64u : 128u;
-    if (!code_map(&p.map_w, qb, N, K, 128u) || !code_map(&p.map_x, qa, M, K, tok)) return cudaErrorInvalidValue;
-    p.sfw = sfb;
+    if (!fill(p, qb, sfb, M, N, K, out, ldd, tok, d_flags) || !code_map(&p.map_x, qa, M, K, tok)) return cudaErrorInvalidValue;
     p.sfx = sfa;
-    p.out = out;
-    p.ldd = ldd;
-    p.M = (uint32_t)M;
-    p.N = (uint32_t)N;
-    p.n_tiles = (uint32_t)((N + 127) / 128);
-    p.stages = (uint32_t)((K + 255) / 256);
-    p.kt = (uint32_t)((K + 127) / 128);
-    p.d_flags = d_flags;
     const uint32_t tiles = p.n_tiles * (uint32_t)((M + tok - 1) / tok);
-    p.z = 1u;
-    while (p.z < 8u && tiles * p.z * 2u <= (uint32_t)num_sms() && p.stages >= 4u * p.z) p.z *= 2u;
     auto pick = [&](auto o) {
         constexpr int O = decltype(o)::value;
         if (tok == 16u) return run<16, O>(p, tiles, dependent, s);
@@ -312,6 +379,19 @@ cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const
         return run<128, O>(p, tiles, dependent, s);
     };
     return out_dt == 2 ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 0>{});
+}
+
+cudaError_t launch_linear_mxfp4_small(const void* x, int in_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
+                                      const uint8_t* sfw, int64_t N, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,
+                                      cudaStream_t s)
+{
+    using namespace gemmx;
+    Params p = {};
+    if (!fill(p, qw, sfw, M, N, K, out, ldd, 16u, d_flags)) return cudaErrorInvalidValue;
+    p.x = x;
+    p.ldx = ldx;
+    if (in_dt == 0) return out_dt == 2 ? run<16, 2, 0>(p, p.n_tiles, false, s) : run<16, 0, 0>(p, p.n_tiles, false, s);
+    return out_dt == 2 ? run<16, 2, 2>(p, p.n_tiles, false, s) : run<16, 0, 2>(p, p.n_tiles, false, s);
 }
 
 }  // namespace nv4

@@ -125,6 +125,11 @@ cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8
 cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
                                     int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, bool dependent,
                                     uint32_t* d_flags, cudaStream_t s);
+// The linear layer for up to kMaxFusedRows rows: quantization and product in one kernel.
+constexpr int64_t kMaxFusedRows = 16;
+cudaError_t launch_linear_mxfp4_small(const void* x, int in_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
+                                      const uint8_t* sfw, int64_t N, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,
+                                      cudaStream_t s);
 cudaError_t launch_dequant(const DequantTask* tasks, int n, int out_dt, cudaStream_t s);
 cudaError_t launch_hessian(const nv4_hessian_job* jobs, int n, uint32_t* d_flags, cudaStream_t s, int* bad_job);
 cudaError_t launch_sweep(const nv4_sweep_job* jobs, int n, int dt, uint32_t* d_flags, cudaStream_t s);

@@ -16,54 +16,11 @@
 
 #include "nv4_common.cuh"
 #include "nv4_internal.h"
+#include "nv4_mxfp4.cuh"
 
 namespace nv4 {
 
 constexpr int kVarThreads = 256;
-
-template <int kIn>
-__device__ __forceinline__ void load16(const void* x, int64_t off, float v[16], uint32_t& amax_bits)
-{
-    amax_bits = 0u;
-    if constexpr (kIn == 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + off);
-        const uint4 a = __ldcs(src), b = __ldcs(src + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t m = 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
-            v[2 * j] = bf16_lo(w[j]);
-            v[2 * j + 1] = bf16_hi(w[j]);
-        }
-        amax_bits = max(m & 0xFFFFu, m >> 16) << 16;
-    } else {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + off);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint4 t = __ldcs(src + k);
-            const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                amax_bits = max(amax_bits, w[j] & 0x7FFFFFFFu);
-                v[4 * k + j] = __uint_as_float(w[j]);
-            }
-        }
-    }
-}
-
-// floor(log2(a)) for a finite positive FP32 bit pattern (normal or subnormal).
-__device__ __forceinline__ int floor_log2_bits(uint32_t b)
-{
-    const int e = (int)(b >> 23);
-    return e != 0 ? e - 127 : -149 + (31 - __clz(b));
-}
-
-// 2^k as FP32 for k in [-149, 127] (exact).
-__device__ __forceinline__ float pow2f(int k)
-{
-    return k >= -126 ? __uint_as_float((uint32_t)(k + 127) << 23) : __uint_as_float(1u << (k + 149));
-}
 
 // ------------------------------------------------------------------ MXFP4
 template <int kIn>
@@ -134,20 +91,9 @@ mxfp4_quant_mma_kernel(const void* x, uint32_t rows, uint32_t cols, uint32_t kt,
         if (live) load16<kIn>(x, (int64_t)r * ld + k, v, ab);
         ab = max(ab, __shfl_xor_sync(0xFFFFFFFFu, ab, 1));
         if (live) {
-            uint32_t c0 = 0u, c1 = 0u;
-            if (ab >= 0x7F800000u) {
-                flags |= kFlagNonFinite;
-                code = 0xFFu;
-            } else {
-                const int e = ab == 0u ? -127 : max(floor_log2_bits(ab) - 2, -127);
-                code = (uint32_t)(e + 127);
-                const float inv = pow2f(-e);
-                float y[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(v[i], inv);
-                c0 = cvt_e2m1x8(y);
-                c1 = cvt_e2m1x8(y + 8);
-            }
+            uint32_t c0, c1;
+            code = mxfp4_encode16(v, ab, c0, c1);
+            if (code == 0xFFu) flags |= kFlagNonFinite;
             *reinterpret_cast<uint2*>(q + (int64_t)r * (cols / 2u) + 8u * hh) = make_uint2(c0, c1);
         }
         uint32_t w = code << (8u * ((lane >> 1) & 3u));

@@ -196,9 +196,9 @@ cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int
     using namespace w4;
     const uint32_t nch = (uint32_t)((K + kChunk - 1) / kChunk);
     uint32_t cap = (uint32_t)(T < 24 ? T : 24), z = 1u;
-    // split K until a CTA stages 128 chunks of token rows, as long as it keeps two chunks of K;
-    // clusters of 8 leave a sixth of the SMs without one (15 fit at once), of 4 hardly any
-    while (z < 4u && cap * nch > 128u * z && nch >= 4u * z) z *= 2u;
+    // split K until a CTA stages 128 chunks of token rows, as long as it keeps two chunks (5 x 2048 x
+    // 16384: 23.7 us unsplit, 11.4 us in clusters of 4; 4 x 2048 x 2048: 4.4 us unsplit, 5.4 split)
+    while (z < 8u && cap * nch > 128u * z && nch >= 4u * z) z *= 2u;
     const uint32_t per = (nch + z - 1u) / z * 512u;                // bytes of a token row in a CTA
     // per 8 tokens: the warps' sums, twice, and a cluster's sums of at least 256 rows
     const size_t sums = (2u * kWarps * 128u + 2048u) * sizeof(float);

@@ -128,7 +128,7 @@ def test_linear_mxfp4_run(orc):
     w = (0.02 * rng.standard_normal((520, 736))).astype(np.float32)
     qw, ew, _ = orc.mxfp4_quant(w)
     dq, ds = G.u8_dev(qw), nv4.mma_scales(G.u8_dev(ew))
-    for M in (1, 33, 270):
+    for M in (1, 7, 16, 33, 270):
         xs = [torch.from_numpy(rng.laplace(size=(M, 736)).astype(np.float32)).to(torch.bfloat16).to(G.DEV) for _ in range(3)]
         want = []
         for x in xs:
@@ -150,7 +150,8 @@ def test_linear_mxfp4_run(orc):
         with torch.cuda.graph(graph):
             nv4.nv4_mxfp4_quant_mma(xin, q, sf)
             nv4.nv4_gemm_mxfp4(q, sf, dq, ds, out)
-        work = torch.full((nv4.nv4_linear_mxfp4_work_bytes(M, 736),), 0xFF, dtype=torch.uint8, device=G.DEV)
+        nb = nv4.nv4_linear_mxfp4_work_bytes(M, 736)
+        work = torch.full((nb,), 0xFF, dtype=torch.uint8, device=G.DEV) if nb else None
         graph2, out2 = torch.cuda.CUDAGraph(), torch.empty_like(out)
         with torch.cuda.graph(graph2):
             nv4.nv4_linear_mxfp4(xin, dq, ds, out2, work)
@@ -161,3 +162,32 @@ def test_linear_mxfp4_run(orc):
             torch.cuda.synchronize()
             assert torch.equal(out, y) and torch.equal(out2, y)
     assert nv4.linear_mxfp4(xs[0][:0], dq, ds).shape == (0, 520)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 32), (3, 130, 288), (15, 300, 2880), (16, 128, 4128), (5, 2000, 544), (2, 64, 16384)])
+def test_linear_quantizes_within_the_product(orc, dt, M, N, K):
+    """Up to 16 rows: the same codes and scales as the quantizer's (the product of its output is
+    the same to the bit), rows inside a wider tensor whose padding holds NaN, zero blocks, blocks
+    far apart in scale."""
+    rng = np.random.default_rng(M * N)
+    x = (rng.laplace(size=(M, K)) * np.exp2(rng.integers(-20, 20, (M, K // 32))).repeat(32, 1)).astype(np.float32)
+    x[:, :32] = 0.0
+    wide = torch.full((M, K + 8), float("nan"), dtype=dt, device=G.DEV)
+    wide[:, :K] = torch.from_numpy(x).to(dt).to(G.DEV)
+    xs = wide[:, :K]
+    qw, ew = operand(rng, N, K)
+    dq, ds = G.u8_dev(qw), nv4.mma_scales(G.u8_dev(ew))
+    for out_dt in (torch.float32, torch.bfloat16):
+        f = G.flags_dev()
+        y = nv4.linear_mxfp4(xs, dq, ds, out_dt, f)
+        q, sf = nv4.mxfp4_quant_mma(xs)
+        assert torch.equal(y, nv4.gemm_mxfp4(q, sf, dq, ds, out_dt)) and f.item() == 0
+    q, e, _ = orc.mxfp4_quant(np.ascontiguousarray(G.host(xs.contiguous())))
+    D, Dabs = orc.gemm_mxfp4(q, e, qw, ew)
+    got = nv4.linear_mxfp4(xs, dq, ds, torch.float32).double().cpu().numpy()
+    assert np.all(np.abs(got - D) <= (K / 64 + 4) * 2.0 ** -23 * Dabs + 2.0 ** -24 * np.abs(D) + 1e-38)
+    xs[M - 1, K - 1] = float("inf")                          # flagged, its row NaN, the others not
+    f = G.flags_dev()
+    y = nv4.linear_mxfp4(xs, dq, ds, torch.float32, f)
+    assert f.item() == nv4.FLAG_NONFINITE and torch.isnan(y[M - 1]).all() and torch.isfinite(y[:M - 1]).all()

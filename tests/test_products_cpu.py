@@ -113,13 +113,16 @@ def test_mxfp4_product_refusals(L):
     assert gemm(qb=FAKE + 8) == 3 and gemm(sa=FAKE + 4) == 3 and gemm(out=FAKE + 8) == 3
     assert gemm(M=0) == 0 and gemm(N=0, ldd=0) == 0 and gemm(M=1 << 31) == 6
 
-    def linear(x=FAKE, dt=0, M=4, K=64, ldx=64, qw=FAKE, sw=FAKE, N=8, odt=0, out=FAKE, ldd=8, work=FAKE, wb=1 << 20):
+    def linear(x=FAKE, dt=0, M=20, K=64, ldx=64, qw=FAKE, sw=FAKE, N=8, odt=0, out=FAKE, ldd=8, work=FAKE, wb=1 << 20):
         return L.nv4_linear_mxfp4(x, dt, M, K, ldx, qw, sw, N, odt, out, ldd, work, wb, None, None)
 
-    assert linear(dt=1) == 4 and linear(odt=1) == 4 and linear(K=48, ldx=48) == 2 and linear(ldx=32) == 2
-    assert linear(x=None) == 1 and linear(qw=None) == 1 and linear(work=None) == 1 and linear(out=FAKE + 8) == 3
-    assert linear(work=FAKE + 8) == 3 and linear(wb=L.nv4_linear_mxfp4_work_bytes(4, 64) - 1) == 6 and linear(M=0) == 0
-    assert L.nv4_linear_mxfp4_work_bytes(4, 64) == 512 + 4 * 32 and L.nv4_linear_mxfp4_work_bytes(0, 64) == 0
+    for M in (4, 20):                                        # within the product, and with a workspace
+        assert linear(M=M, dt=1) == 4 and linear(M=M, odt=1) == 4 and linear(M=M, K=48, ldx=48) == 2 and linear(M=M, ldx=32) == 2
+        assert linear(M=M, x=None) == 1 and linear(M=M, qw=None) == 1 and linear(M=M, out=FAKE + 8) == 3
+        assert linear(M=M, x=FAKE + 8) == 3 and linear(M=M, ldx=68) == 3 and linear(M=M, ldd=7) == 2 and linear(M=M, K=0) == 2
+    assert linear(work=None) == 1 and linear(work=FAKE + 8) == 3 and linear(M=0) == 0
+    assert linear(wb=L.nv4_linear_mxfp4_work_bytes(20, 64) - 1) == 6
+    assert L.nv4_linear_mxfp4_work_bytes(20, 64) == 512 + 20 * 32 and L.nv4_linear_mxfp4_work_bytes(16, 64) == 0
     assert L.nv4_mxfp4_mma_scale_bytes(200, 288) == 256 * 12 and L.nv4_mxfp4_mma_scale_bytes(1, 32) == 512
     assert L.nv4_mxfp4_mma_scale_bytes(4, 48) == 0 and L.nv4_mxfp4_mma_scale_bytes(0, 32) == 0
 
