@@ -12,8 +12,8 @@
 //   * warp 1: owns the tensor memory; one lane issues four MMAs (K = 64) per stage.
 //   * warps 4-7: move the scales into tensor memory (tcgen05.st, see gemm.cu), then read the
 //     accumulator, one weight row per thread.
-//   * warps 8-11, where x comes unquantized (the linear layer, up to 16 rows): quantize their CTA's
-//     part of x into the stage, codes in the swizzled layout and scales as atoms, one stage ahead.
+//   * warps 8-15, where x comes unquantized (the linear layer, up to 16 rows): quantize their CTA's
+//     part of x into the stage, codes in the swizzled layout and scales as atoms, three stages ahead.
 //     One launch instead of two, and no workspace.
 // Every mbarrier wait is bounded (kWaitLimitNs), as in gemm.cu.
 #include <type_traits>
@@ -29,7 +29,8 @@ namespace gemmx {
 
 using namespace tc;
 
-constexpr int kThreads = 256;                     // + 128 that quantize
+constexpr int kThreads = 256;                     // + those that quantize
+constexpr int kQuant = 256;
 constexpr int kStages = 6;
 constexpr int kSfBufs = 4;                        // 16 columns each: 8 of the weights, 8 of the rows
 constexpr uint32_t kSfCol = 128;                  // behind the accumulator
@@ -62,13 +63,13 @@ struct Smem {
 
 // kIn: -1 A quantized, else the type of x (0 BF16, 2 FP32).
 template <int kTok, int kOut, int kIn>
-__global__ void __launch_bounds__(kIn >= 0 ? kThreads + 128 : kThreads, 1) gemm_mx_small_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kIn >= 0 ? kThreads + kQuant : kThreads, 1) gemm_mx_small_kernel(const __grid_constant__ Params p)
 {
     // kind::mxf4: A and B E2M1, K-major, E8M0 scales (bit 23), N >> 3 in bits 17-22, M >> 4 in bits
     // 24-28; the two bytes of a scale word that a step uses in bits 4-5 (B) and 29-30 (A)
     constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kTok >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
     constexpr uint32_t kTx = 128u * 128u + 1024u + (kIn >= 0 ? 0u : kTok * 128u + 1024u);
-    constexpr uint32_t kBlock = kIn >= 0 ? kThreads + 128 : kThreads;
+    constexpr uint32_t kBlock = kIn >= 0 ? kThreads + kQuant : kThreads;
     extern __shared__ uint8_t smem_raw[];
     Smem<kTok>& sm = *reinterpret_cast<Smem<kTok>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kIn >= 0 ? kThreads + 128 : kThreads, 1) gemm_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[s], kIn >= 0 ? 1 + 4 : 1);          // the copies, the quantizing warps
+            mbar_init(&sm.full[s], kIn >= 0 ? 1 + kQuant / 32 : 1);          // the copies, the quantizing warps
             mbar_init(&sm.empty[s], 1);
         }
         for (int b = 0; b < kSfBufs; ++b) {
@@ -169,21 +170,22 @@ __global__ void __launch_bounds__(kIn >= 0 ? kThreads + 128 : kThreads, 1) gemm_
         if constexpr (kIn >= 0) {
             const uint32_t tid = threadIdx.x - kThreads;
             const uint32_t kb = ks0 * 256u;
-            constexpr uint32_t kPer = kTok * 16u / 128u;           // half blocks per thread
-            float v[kPer][16];
-            uint32_t ab[kPer];
-            auto fetch = [&](uint32_t ks) {
+            constexpr uint32_t kPer = kTok * 16u / kQuant;         // half blocks per thread
+            constexpr uint32_t kAhead = 3;                         // stages of x in registers
+            float vs[kAhead][kPer][16];
+            uint32_t abs_[kAhead][kPer];
+            auto fetch = [&](float (&v)[kPer][16], uint32_t (&ab)[kPer], uint32_t ks) {
 #pragma unroll
                 for (uint32_t j = 0; j < kPer; ++j) {
-                    const uint32_t i = tid + 128u * j, r = i >> 4, k = kb + 256u * ks + 16u * (i & 15u);
+                    const uint32_t i = tid + kQuant * j, r = i >> 4, k = kb + 256u * ks + 16u * (i & 15u);
                     ab[j] = 0u;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[j][e] = 0.0f;
                     if (r < p.M - m0 && k < p.K && ks < KS) load16<kIn>(p.x, (int64_t)(m0 + r) * p.ldx + k, v[j], ab[j]);
                 }
             };
-            fetch(0u);
-            for (uint32_t ks = 0; ks < KS; ++ks) {
+            bool stop = false;
+            auto stage = [&](float (&v)[kPer][16], uint32_t (&ab)[kPer], uint32_t ks) {
                 const uint32_t s = ks % kStages;
                 uint32_t code[kPer], c0[kPer], c1[kPer];
 #pragma unroll
@@ -192,15 +194,16 @@ __global__ void __launch_bounds__(kIn >= 0 ? kThreads + 128 : kThreads, 1) gemm_
                     code[j] = mxfp4_encode16(v[j], ab[j], c0[j], c1[j]);
                     if (code[j] == 0xFFu) flags |= kFlagNonFinite;
                 }
-                fetch(ks + 1u);
+                fetch(v, ab, ks + kAhead);
                 const bool ok = ks < (uint32_t)kStages || wait_bar(&sm.empty[s], ((ks / kStages) - 1u) & 1u);
                 if (!__all_sync(0xFFFFFFFFu, ok) || __any_sync(0xFFFFFFFFu, aborted())) {
                     if (!ok && lane == 0) give_up();
-                    break;
+                    stop = true;
+                    return;
                 }
 #pragma unroll
                 for (uint32_t j = 0; j < kPer; ++j) {
-                    const uint32_t i = tid + 128u * j, r = i >> 4, h = i & 15u;        // half block h of row r: block h / 2
+                    const uint32_t i = tid + kQuant * j, r = i >> 4, h = i & 15u;        // half block h of row r: block h / 2
                     *reinterpret_cast<uint2*>(sm.x[s] + 128u * r + 16u * ((h >> 1) ^ (r & 7u)) + 8u * (h & 1u)) =
                         make_uint2(c0[j], c1[j]);
                     if ((h & 1u) == 0u) sm.sfx[s][512u * (h >> 3) + 16u * r + ((h >> 1) & 3u)] = (uint8_t)code[j];
@@ -208,7 +211,13 @@ __global__ void __launch_bounds__(kIn >= 0 ? kThreads + 128 : kThreads, 1) gemm_
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.full[s]);
-            }
+            };
+#pragma unroll
+            for (uint32_t a = 0; a < kAhead; ++a) fetch(vs[a], abs_[a], a);
+            for (uint32_t ks = 0; ks < KS && !stop; ks += kAhead)
+#pragma unroll
+                for (uint32_t a = 0; a < kAhead; ++a)
+                    if (ks + a < KS && !stop) stage(vs[a], abs_[a], ks + a);
             __syncwarp();
         }
     } else if (warp >= 4) {
@@ -316,7 +325,7 @@ static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStre
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.z, 1, 1);
-    cfg.blockDim = dim3(kIn >= 0 ? kThreads + 128 : kThreads, 1, 1);
+    cfg.blockDim = dim3(kIn >= 0 ? kThreads + kQuant : kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
