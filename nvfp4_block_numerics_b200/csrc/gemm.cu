@@ -597,17 +597,30 @@ gemm_pair_kernel(const __grid_constant__ Params p)
                 for (int cb = 0; cb < 4; ++cb) {
                     float v[32];
                     tmem_ld32(taddr + (uint32_t)(32 * cb), v);
+                    if (kMx && (p.vec == 0u || col0 + 32 * cb + 32 > p.N)) {
+                        // as for BF16 below: through shared memory, 4 rows x 8 columns a store
+                        float* sf = reinterpret_cast<float*>(st);
+#pragma unroll
+                        for (int c8 = 0; c8 < 4; ++c8) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) sf[8 * lane + ((k + lane) & 7)] = v[8 * c8 + k];
+                            __syncwarp();
+                            const int c = lane & 7;
+                            const int64_t col = col0 + 32 * cb + 8 * c8 + c;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int rr = 4 * k + (lane >> 3);
+                                if (row0 + rr < p.M && col < p.N)
+                                    static_cast<float*>(p.out)[(row0 + rr) * p.ldd + col] = sf[8 * rr + ((c + rr) & 7)];
+                            }
+                            __syncwarp();
+                        }
+                        continue;
+                    }
                     float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (row0 + lane) * p.ldd + col0 + 32 * cb);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int64_t col = col0 + 32 * cb + 4 * k;
-                        if (kMx && (row0 + lane >= p.M || col + 4 > p.N || p.vec == 0u)) {
-                            if (row0 + lane < p.M)
-                                for (int i2 = 0; i2 < 4; ++i2)
-                                    if (col + i2 < p.N)
-                                        static_cast<float*>(p.out)[(row0 + lane) * p.ldd + col + i2] = v[4 * k + i2];
-                            continue;
-                        }
+                        if (kMx && row0 + lane >= p.M) continue;
                         o[k] = make_float4(__fmul_rn(v[4 * k], alpha), __fmul_rn(v[4 * k + 1], alpha),
                                            __fmul_rn(v[4 * k + 2], alpha), __fmul_rn(v[4 * k + 3], alpha));
                     }
@@ -635,22 +648,25 @@ gemm_pair_kernel(const __grid_constant__ Params p)
                             make_uint4(w[8 * c16 + 4 * k], w[8 * c16 + 4 * k + 1], w[8 * c16 + 4 * k + 2],
                                        w[8 * c16 + 4 * k + 3]);
                     __syncwarp();
+                    if (kMx && (p.vec == 0u || col0 + 16 * c16 + 16 > p.N)) {
+                        // rows of no 16-byte alignment, or the ragged end: 2 rows x 16 columns a store
+                        const int c = lane & 15;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int rr = 2 * k + (lane >> 4);
+                            const int64_t col = col0 + 16 * c16 + c;
+                            if (row0 + rr < p.M && col < p.N)
+                                static_cast<uint16_t*>(p.out)[(row0 + rr) * p.ldd + col] = *reinterpret_cast<const uint16_t*>(
+                                    st + 32 * rr + 16 * ((c >> 3) ^ ((rr >> 2) & 1)) + 2 * (c & 7));
+                        }
+                        __syncwarp();
+                        continue;
+                    }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int rr = pr + 16 * k;
                         const uint4 x = *reinterpret_cast<const uint4*>(st + 32 * rr + 16 * (pc ^ ((rr >> 2) & 1)));
-                        const int64_t col = col0 + 16 * c16 + 8 * pc;
-                        if (kMx && (row0 + rr >= p.M || col + 8 > p.N || p.vec == 0u)) {
-                            if (row0 + rr < p.M) {
-                                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int i2 = 0; i2 < 8; ++i2)
-                                    if (col + i2 < p.N)
-                                        static_cast<uint16_t*>(p.out)[(row0 + rr) * p.ldd + col + i2] =
-                                            (uint16_t)(xw[i2 >> 1] >> (16 * (i2 & 1)));
-                            }
-                            continue;
-                        }
+                        if (kMx && row0 + rr >= p.M) continue;
                         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row0 + rr) * p.ldd + col0 + 16 * c16 +
                                                   8 * pc) = x;
                     }

@@ -107,6 +107,17 @@ def test_gemm_output_strides(orc, M, dt):
         assert torch.all(dst[:, 203:] == 9.0)
 
 
+@pytest.mark.parametrize("M,N,pad", [(517, 515, 0), (517, 515, 5), (300, 769, 0), (517, 514, 2), (259, 512, 1)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gemm_unaligned_rows_of_tall_products(orc, M, N, pad, dt):
+    """Several tiles of the tall kernel with an odd row pitch, a ragged last tile, or both; what lies
+    between the rows stays as it was."""
+    rng = np.random.default_rng(M + N + pad)
+    dst = torch.full((M, N + pad), 9.0, dtype=dt, device=G.DEV)
+    check(orc, *operand(rng, M, 288), *operand(rng, N, 288), dtypes=(dt,), out=dst[:, :N])
+    assert torch.all(dst[:, N:] == 9.0)
+
+
 @pytest.mark.parametrize("M", [4, 260])
 def test_gemm_nan_scales_stay_in_their_rows(orc, M):
     rng = np.random.default_rng(4)
