@@ -892,8 +892,8 @@ def moe_layer(x, w_router, gate, up, down, top_k: int, renormalize=True, dtype=N
     """The whole layer: x [T, H] -> (out [T, H], ids, weights)."""
     T, H = x.shape
     out = _new((T, H), dtype or x.dtype, x, stream)
-    routing = _new((2, T, top_k), torch.int32, x, stream)
-    ids, weights = routing[0], routing[1].view(torch.float32)
+    ids = _new((T, top_k), torch.int32, x, stream)
+    weights = _new((T, top_k), torch.float32, x, stream)
     work = _new((nv4_moe_work_bytes(T, top_k, H, gate[0].shape[1]),), torch.uint8, x, stream)
     nv4_moe_layer(x, w_router, gate, up, down, ids, weights, out, work, renormalize, d_flags, stream)
     return out, ids, weights
