@@ -767,7 +767,7 @@ def _rows16(x: torch.Tensor, name: str):
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise NV4Error(f"{name} must be bf16 or float16")
     rows, cols, ld = _rowmajor(x, name)
-    return rows, cols, max(ld, cols) if rows <= 1 else ld
+    return rows, cols, cols if rows <= 1 else ld
 
 
 def nv4_linear_w4a16(x, q, scales, d_s2, out, d_flags=None, stream=None):
@@ -918,7 +918,7 @@ def nv4_mxfp4_quant_mma(x, q, e8m0_mma, d_flags=None, stream=None):
     rows, cols, ld = _rowmajor(x, "x")
     _bytes(q, (rows, cols // 2), "q")
     _mma_bytes(e8m0_mma, rows, cols, "e8m0_mma")
-    _check(lib().nv4_mxfp4_quant_mma(x.data_ptr(), _DT[x.dtype], rows, cols, max(ld, cols) if rows <= 1 else ld,
+    _check(lib().nv4_mxfp4_quant_mma(x.data_ptr(), _DT[x.dtype], rows, cols, cols if rows <= 1 else ld,
                                      q.data_ptr(), e8m0_mma.data_ptr(), _ptr(d_flags), _on(stream, dev)),
            "nv4_mxfp4_quant_mma")
 
@@ -977,7 +977,7 @@ def nv4_linear_mxfp4(x, qw, sfw_mma, out, work=None, d_flags=None, stream=None):
     if work is not None and not work.is_contiguous():
         raise NV4Error("work must be contiguous")
     _mma_bytes(sfw_mma, N, K, "sfw_mma")
-    _check(lib().nv4_linear_mxfp4(x.data_ptr(), _DT[x.dtype], M, K, max(ldx, K) if M <= 1 else ldx,
+    _check(lib().nv4_linear_mxfp4(x.data_ptr(), _DT[x.dtype], M, K, K if M <= 1 else ldx,
                                   _bytes(qw, (N, K // 2), "qw"), sfw_mma.data_ptr(), N, _DT[out.dtype], out.data_ptr(),
                                   max(ldd, N) if M <= 1 else ldd, None if work is None else work.data_ptr(),
                                   0 if work is None else work.numel() * work.element_size(), _ptr(d_flags),

@@ -727,7 +727,8 @@ static cudaError_t run_pair(const Params& p, int dev, cudaStream_t s)
 {
     static bool attr_set[64] = {};
     static int resident[64] = {};
-    const size_t smem = sizeof(Smem2) + 1024;
+    constexpr size_t smem = sizeof(Smem2) + 1024;
+    static_assert(smem > kSmemOfOnePerSm, "one CTA per SM: see kSmemOfOnePerSm");
     auto kern = gemm_pair_kernel<kMx, kOut>;
     const bool known = dev >= 0 && dev < 64;
     if (!known || !attr_set[dev]) {
@@ -839,8 +840,8 @@ cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8
                               uint32_t* d_flags, cudaStream_t s)
 {
     using namespace gemm;
-    // few rows: the rows of B fill the tensor cores' 128 rows (gemm_mx.cu)
-    if (M <= 128) return launch_gemm_mxfp4_small(qa, sfa, qb, sfb, M, N, K, out_dt, out, ldd, dependent, d_flags, s);
+    // few rows, or few tiles: the kernel of 128-row tiles, which splits K (gemm_mx.cu)
+    if (M <= kMaxSmallRows || ((M + 127) / 128) * ((N + 127) / 128) <= num_sms()) return launch_gemm_mxfp4_small(qa, sfa, qb, sfb, M, N, K, out_dt, out, ldd, dependent, d_flags, s);
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

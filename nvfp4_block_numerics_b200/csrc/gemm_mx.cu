@@ -1,15 +1,17 @@
-// gemm_mx.cu -- MXFP4 x MXFP4 product for few rows of A (decode batches), on the block-scaled
-// tensor cores (sm_100a).  The form for many rows is the CTA-pair kernel of gemm.cu.
+// gemm_mx.cu -- MXFP4 x MXFP4 product for few rows of A (decode batches) or few tiles, on the
+// block-scaled tensor cores (sm_100a).  The form for many is the CTA-pair kernel of gemm.cu.
 //
 // [FP4] 1.2, 4.1.  D^T tile = B tile * A tile^T: 128 rows of B (the weights) are the MMA's M, up to
 // kTok rows of A its N, so that the tensor cores' 128 rows are filled by the operand that has them.
 // The bound is reading the weights once: N x K x 17/32 bytes.  One tile per cluster of z CTAs, each
-// with its own part of K (z up to 8 where there are fewer tiles than SMs); the partial sums meet
+// with its own part of K (nv4_split.h; 16 x 2048 x 16384: 14.0 us with z = 8 in two waves, 9.0
+// with z = 6 in one); the partial sums meet
 // through distributed shared memory, added in rank order.
 //   * warp 0, one lane: TMA of the code tiles (256 K-elements per stage, 128-byte swizzle, zeros
 //     outside) and bulk copies of the scale atoms.  The first stages' weights are requested before
 //     the wait for the kernel in front (programmatic dependent launch), the rows of A after it.
-//   * warp 1: owns the tensor memory; one lane issues four MMAs (K = 64) per stage.
+//   * warp 1: owns the tensor memory; walks the stages with all lanes and issues four MMAs (K = 64)
+//     per stage from an elected one.
 //   * warps 4-7: move the scales into tensor memory (tcgen05.st, see gemm.cu), then read the
 //     accumulator, one weight row per thread.
 //   * warps 8-15, where x comes unquantized (the linear layer, up to 16 rows): quantize their CTA's
@@ -20,6 +22,7 @@
 
 #include "nv4_internal.h"
 #include "nv4_mxfp4.cuh"
+#include "nv4_split.h"
 #include "nv4_tcgen05.cuh"
 #include "nv4_tensormap.h"
 
@@ -276,27 +279,25 @@ __global__ void __launch_bounds__(kIn >= 0 ? kThreads + kQuant : kThreads, 1) ge
     if (p.z > 1u) cluster_sync();
     if (!aborted()) {
         const uint32_t n0 = n_tile * 128u, rows = min(128u, p.N - n0), toks = min((uint32_t)kTok, p.M - m0);
-        const uint32_t j1 = (rank + 1u) * toks * 128u / p.z;
-        for (uint32_t i = rank * toks * 128u / p.z + threadIdx.x; i < j1; i += kBlock) {
-            const uint32_t r = i & 127u, tok = i >> 7;
+        // four weight rows of a row of A per thread
+        const uint32_t j1 = (rank + 1u) * toks * 32u / p.z;
+        for (uint32_t i = rank * toks * 32u / p.z + threadIdx.x; i < j1; i += kBlock) {
+            const uint32_t r = 4u * (i & 31u), tok = i >> 5;
             if (r >= rows) continue;
-            float sum = 0.0f;
-            if (p.z > 1u) {
-                float v[8];
-#pragma unroll
-                for (uint32_t k = 0; k < 8u; ++k) v[k] = k < p.z ? ld_dsmem_f32(&sm.part[0][0] + i, k) : 0.0f;
-#pragma unroll
-                for (uint32_t k = 0; k < 8u; ++k) sum += v[k];
-            } else {
-                sum = sm.part[tok][r];
-            }
+            const float* own = &sm.part[0][0] + 4u * i;
+            const float4 v = p.z > 1u ? cluster_sum4(own, p.z) : *reinterpret_cast<const float4*>(own);
+            const float sum[4] = {v.x, v.y, v.z, v.w};
             const int64_t at = (int64_t)(m0 + tok) * p.ldd + n0 + r;
-            if constexpr (kOut == 2) {
-                static_cast<float*>(p.out)[at] = sum;
-            } else {
-                uint16_t b;
-                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(sum));
-                static_cast<uint16_t*>(p.out)[at] = b;
+#pragma unroll
+            for (uint32_t k = 0; k < 4u; ++k) {
+                if (r + k >= rows) break;
+                if constexpr (kOut == 2) {
+                    static_cast<float*>(p.out)[at + k] = sum[k];
+                } else {
+                    uint16_t b;
+                    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(sum[k]));
+                    static_cast<uint16_t*>(p.out)[at + k] = b;
+                }
             }
         }
     }
@@ -310,11 +311,13 @@ __global__ void __launch_bounds__(kIn >= 0 ? kThreads + kQuant : kThreads, 1) ge
 }
 
 template <int kTok, int kOut, int kIn = -1>
-static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStream_t s)
+static cudaError_t run(Params& p, uint32_t tiles, bool dependent, cudaStream_t s)
 {
     static bool ready[64] = {};
+    static int fits[64][kMaxSplit + 1] = {};
     auto kern = gemm_mx_small_kernel<kTok, kOut, kIn>;
-    const size_t smem = sizeof(Smem<kTok>) + 1024;
+    constexpr size_t smem = sizeof(Smem<kTok>) + 1024;
+    static_assert(smem > kSmemOfOnePerSm, "one CTA per SM: see kSmemOfOnePerSm");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -323,9 +326,12 @@ static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStre
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
+    constexpr int threads = kIn >= 0 ? kThreads + kQuant : kThreads;
+    // a wave beside its stages (launch, first loads, the cluster's sums): some 4 stages' time
+    p.z = split_tiles(kern, threads, smem, tiles, p.stages, 2u, 4u, fits, dev);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.z, 1, 1);
-    cfg.blockDim = dim3(kIn >= 0 ? kThreads + kQuant : kThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -348,7 +354,7 @@ static cudaError_t run(const Params& p, uint32_t tiles, bool dependent, cudaStre
 }
 
 static bool fill(Params& p, const uint8_t* qw, const uint8_t* sfw, int64_t M, int64_t N, int64_t K, void* out, int64_t ldd,
-                 uint32_t tok, uint32_t* d_flags)
+                 uint32_t* d_flags)
 {
     if (!code_map(&p.map_w, qw, N, K, 128u)) return false;
     p.sfw = sfw;
@@ -361,10 +367,6 @@ static bool fill(Params& p, const uint8_t* qw, const uint8_t* sfw, int64_t M, in
     p.stages = (uint32_t)((K + 255) / 256);
     p.kt = (uint32_t)((K + 127) / 128);
     p.d_flags = d_flags;
-    // split K in clusters while there are SMs for it and every CTA keeps two stages
-    const uint32_t tiles = p.n_tiles * (uint32_t)((M + tok - 1) / tok);
-    p.z = 1u;
-    while (p.z < 8u && tiles * p.z * 2u <= (uint32_t)num_sms() && p.stages >= 4u * p.z) p.z *= 2u;
     return true;
 }
 
@@ -377,7 +379,7 @@ cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const
     using namespace gemmx;
     Params p = {};
     const uint32_t tok = M <= 16 ? 16u : M <= 32 ? 32u : M <= 64 ? 64u : 128u;
-    if (!fill(p, qb, sfb, M, N, K, out, ldd, tok, d_flags) || !code_map(&p.map_x, qa, M, K, tok)) return cudaErrorInvalidValue;
+    if (!fill(p, qb, sfb, M, N, K, out, ldd, d_flags) || !code_map(&p.map_x, qa, M, K, tok)) return cudaErrorInvalidValue;
     p.sfx = sfa;
     const uint32_t tiles = p.n_tiles * (uint32_t)((M + tok - 1) / tok);
     auto pick = [&](auto o) {
@@ -396,7 +398,7 @@ cudaError_t launch_linear_mxfp4_small(const void* x, int in_dt, int64_t M, int64
 {
     using namespace gemmx;
     Params p = {};
-    if (!fill(p, qw, sfw, M, N, K, out, ldd, 16u, d_flags)) return cudaErrorInvalidValue;
+    if (!fill(p, qw, sfw, M, N, K, out, ldd, d_flags)) return cudaErrorInvalidValue;
     p.x = x;
     p.ldx = ldx;
     if (in_dt == 0) return out_dt == 2 ? run<16, 2, 0>(p, p.n_tiles, false, s) : run<16, 0, 0>(p, p.n_tiles, false, s);

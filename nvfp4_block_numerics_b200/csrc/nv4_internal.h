@@ -89,6 +89,10 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* qa, const uint8_t* sfa, const float
 // K of one linear_w4a16 / mixture-of-experts call at most: one token row in shared memory.
 constexpr int64_t kMaxW4K = 65536;
 constexpr size_t kMaxSmemW4 = 220u * 1024u;
+// Rows up to which the weight-only linear layer runs on launch_linear_w4a16, above them on its _mma
+// form.  16 rows on either (us): 2880 x 2880 8.8 / 9.9, 16384 x 2048 11.1 / 15.3, 8192 x 8192 23.4 /
+// 27.5; a third column of 8 tokens would cost the former what the latter's 32 columns have free.
+constexpr int64_t kMaxFewRows = 16;
 cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
                                 cudaStream_t s);
@@ -125,7 +129,14 @@ cudaError_t launch_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa, const uint8
 cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb, int64_t M,
                                     int64_t N, int64_t K, int out_dt, void* out, int64_t ldd, bool dependent,
                                     uint32_t* d_flags, cudaStream_t s);
-// The linear layer for up to kMaxFusedRows rows: quantization and product in one kernel.
+// Rows of A up to which launch_gemm_mxfp4 runs on launch_gemm_mxfp4_small (and above them while its
+// 128 x 128 tiles fit the SMs at once), else on the CTA-pair kernel.  Either, in us: 128 x 2880 x 2880
+// 8.5 / 15.7, 128 x 16384 x 2048 10.2 / 11.6, 128 x 8192 x 8192 14.9 / 25.9, 256 x 2048 x 16384 14.6 /
+// 45, 1024 x 2048 x 2048 10.0 / 11.4.
+constexpr int64_t kMaxSmallRows = 128;
+// The linear layer for up to kMaxFusedRows rows: quantization and product in one kernel.  On the
+// device it is level with two (16 x 16384 x 2048 9.3 us, 16 x 2880 x 2880 7.0); a call costs one launch
+// less (1 x 2880 x 2880: 12.5 us a call, 17.5 with two).
 constexpr int64_t kMaxFusedRows = 16;
 cudaError_t launch_linear_mxfp4_small(const void* x, int in_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
                                       const uint8_t* sfw, int64_t N, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,

@@ -30,6 +30,7 @@
 #include "nv4_async.cuh"
 #include "nv4_common.cuh"
 #include "nv4_cpasync.cuh"
+#include "nv4_internal.h"
 
 namespace nv4 {
 namespace w4 {
@@ -198,7 +199,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 // accumulator, and with one chain of 16 per chunk that latency, not the decoding, set the pace
 // (156 clocks per chunk and SM with one chain, T = 5, K = 16384).
 template <int NT>
-constexpr int kChains = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+constexpr int kChains = NT == 1 ? 4 : 2;
 
 template <int NT, int kCh>
 using AccOf = float[kCh][NT][4];
@@ -293,8 +294,8 @@ __host__ __device__ inline uint32_t padded(uint32_t K) { return (K + kChunk - 1u
 // ---------------------------------------------------------------- token rows into shared memory
 // Per token of a pass: exponent statistics and the factor that undoes its scaling.
 struct Rows {
-    uint32_t emax[24], emin[24];                  // largest / smallest non-zero BF16 magnitude bits
-    float descale[24];
+    uint32_t emax[kMaxFewRows], emin[kMaxFewRows];          // largest / smallest non-zero BF16 magnitude bits
+    float descale[kMaxFewRows];
 };
 
 // 2^k for a biased exponent field, clamped to what FP32 holds from above (254) and, as the

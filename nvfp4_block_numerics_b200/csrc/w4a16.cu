@@ -7,8 +7,9 @@
 // One CTA per SM; a cluster of z of them owns a contiguous range of weight rows (balanced to one
 // row) and splits K, each CTA taking its chunks of it: staging the token rows costs a CTA
 // T * K / z values, so z grows with T * K.  A CTA walks its rows in tiles of at most 16; its 16
-// warps split the tiles and, within a tile, K (nv4_w4.cuh).  A weight byte is read once per pass of up to 24 tokens.  The cluster's partial sums
-// meet through distributed shared memory, added in rank order.
+// warps split the tiles and, within a tile, K (nv4_w4.cuh).  A weight byte is read once, unless K
+// is so long that shared memory does not hold all token rows: then once per pass over as many as
+// it holds.  The cluster's partial sums meet through distributed shared memory, added in rank order.
 #include "nv4_async.cuh"
 #include "nv4_internal.h"
 #include "nv4_w4.cuh"
@@ -180,11 +181,8 @@ static cudaError_t run_linear(LinearParams p, cudaStream_t s)
 template <int kDt, int kOut>
 static cudaError_t pick_linear(const LinearParams& p, bool vec, cudaStream_t s)
 {
-    const uint32_t nt = (p.cap + 7u) / 8u;
-    if (vec) return nt == 1 ? run_linear<kDt, kOut, true, 1>(p, s)
-                            : nt == 2 ? run_linear<kDt, kOut, true, 2>(p, s) : run_linear<kDt, kOut, true, 3>(p, s);
-    return nt == 1 ? run_linear<kDt, kOut, false, 1>(p, s)
-                   : nt == 2 ? run_linear<kDt, kOut, false, 2>(p, s) : run_linear<kDt, kOut, false, 3>(p, s);
+    if (vec) return p.cap <= 8u ? run_linear<kDt, kOut, true, 1>(p, s) : run_linear<kDt, kOut, true, 2>(p, s);
+    return p.cap <= 8u ? run_linear<kDt, kOut, false, 1>(p, s) : run_linear<kDt, kOut, false, 2>(p, s);
 }
 
 }  // namespace w4
@@ -195,7 +193,7 @@ cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int
 {
     using namespace w4;
     const uint32_t nch = (uint32_t)((K + kChunk - 1) / kChunk);
-    uint32_t cap = (uint32_t)(T < 24 ? T : 24), z = 1u;
+    uint32_t cap = (uint32_t)T, z = 1u;                            // T is at most kMaxFewRows
     // split K until a CTA stages 128 chunks of token rows, as long as it keeps two chunks (5 x 2048 x
     // 16384: 23.7 us unsplit, 11.4 us in clusters of 4; 4 x 2048 x 2048: 4.4 us unsplit, 5.4 split)
     while (z < 8u && cap * nch > 128u * z && nch >= 4u * z) z *= 2u;

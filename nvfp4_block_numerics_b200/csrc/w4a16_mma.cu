@@ -11,7 +11,8 @@
 // Persistent, one CTA per SM, 20 warps:
 //   * warp 0, one lane: 2-D TMA of x, kTok rows x 64 K-elements per stage (128-byte swizzle, zeros
 //     outside), a ring of kStages that runs across tiles.
-//   * warp 1: owns the tensor memory; one lane issues four MMAs (K = 16) per stage.
+//   * warp 1: owns the tensor memory; walks the stages with all lanes and issues four MMAs (K = 16)
+//     per stage from an elected one.
 //   * warps 4-11: decoders, two sets of four; a warp owns 32 weight rows (the tensor memory lanes
 //     it may write) and takes every other 256-element chunk of K.  It fills a ring in shared memory
 //     for itself with cp.async, eight lanes to a row's 128 bytes, across the ends of tiles; then
@@ -27,6 +28,7 @@
 
 #include "nv4_cpasync.cuh"
 #include "nv4_internal.h"
+#include "nv4_split.h"
 #include "nv4_tcgen05.cuh"
 #include "nv4_tensormap.h"
 
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA issuer
-        // two stages at a time, so that their four barriers are tried together (kStages and kABufs are
-        // even, but a tile may end on an odd stage: the positions are counted over all tiles)
+        // two stages at a time, so that their four barriers are tried together (a tile may end on an
+        // odd stage: the positions are counted over all tiles)
         const uint64_t desc0 = smem_desc(smem_u32(sm.x[0]), 1u, 64u, 2u);
         uint32_t g = 0u, i = 0u;
         bool ok = true;
@@ -421,16 +423,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         const uint32_t n0 = (clu % p.n_tiles) * 128u, tok0 = (clu / p.n_tiles) * kTok;
         const float s2 = *p.d_s2;
         const uint32_t rows = min(128u, p.N - n0), toks = min((uint32_t)kTok, p.T - tok0);
+        // four weight rows of a token per thread
         const uint32_t j1 = (rank + 1u) * toks / p.z;
-        for (uint32_t i = (rank * toks / p.z) * 128u + threadIdx.x; i < j1 * 128u; i += kThreads) {
-            const uint32_t r = i & 127u, tok = i >> 7;
+        for (uint32_t i = (rank * toks / p.z) * 32u + threadIdx.x; i < j1 * 32u; i += kThreads) {
+            const uint32_t r = 4u * (i & 31u), tok = i >> 5;
             if (r >= rows) continue;
-            float v[8], sum = 0.0f;
+            const float4 sum = cluster_sum4(part + 4u * i, p.z);
+            const float o[4] = {sum.x * s2, sum.y * s2, sum.z * s2, sum.w * s2};
+            if (aborted()) continue;
 #pragma unroll
-            for (uint32_t k = 0; k < 8u; ++k) v[k] = k < p.z ? ld_dsmem_f32(part + i, k) : 0.0f;
-#pragma unroll
-            for (uint32_t k = 0; k < 8u; ++k) sum += v[k];
-            if (!aborted()) store1<kOut>(p.out, (int64_t)(tok0 + tok) * p.ldd + n0 + r, sum * s2);
+            for (uint32_t k = 0; k < 4u; ++k)
+                if (r + k < rows) store1<kOut>(p.out, (int64_t)(tok0 + tok) * p.ldd + n0 + r + k, o[k]);
         }
         cluster_sync();                                            // the others have read this CTA's sums
     }
@@ -456,12 +459,14 @@ static bool x_map(CUtensorMap* map, const void* x, int dt, int64_t T, int64_t K,
 }
 
 template <int kTok, int kDt, int kOut, bool kVec>
-static cudaError_t run(const Params& p, cudaStream_t s)
+static cudaError_t run(Params& p, cudaStream_t s)
 {
     static bool ready[64] = {};
+    static int fits[64][kMaxSplit + 1] = {};
     auto kern = linear_mma_kernel<kTok, kDt, kOut, kVec>;
     static_assert(kTok == 256 || kStages<kTok> * 128 >= 512, "the partial sums take the place of x");
     constexpr size_t smem = sizeof(Smem<kTok>) + 1024;
+    static_assert(smem > kSmemOfOnePerSm, "one CTA per SM: see kSmemOfOnePerSm");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -470,8 +475,13 @@ static cudaError_t run(const Params& p, cudaStream_t s)
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
     const uint32_t sms = (uint32_t)num_sms();
+    // every CTA keeps a chunk; a wave beside its chunks (launch, first loads, the cluster's sums): some
+    // 3 chunks' time.  With more tiles than SMs a CTA walks several unsplit, the next one's loads under
+    // the last one's stores (1000 x 2880 x 2880, 184 tiles: 38 us, 52 in clusters of 2).  (The sums of
+    // 256 token columns would leave nothing of x's stages to spare.)
+    p.z = kTok <= 128 && p.tiles <= sms ? split_tiles(kern, kThreads, smem, p.tiles, p.chunks, 1u, 3u, fits, dev) : 1u;
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.z > 1u ? p.tiles * p.z : p.tiles < sms ? p.tiles : sms, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -487,7 +497,7 @@ static cudaError_t run(const Params& p, cudaStream_t s)
 }
 
 template <int kTok>
-static cudaError_t pick(const Params& p, int dt, int out_dt, bool vec, cudaStream_t s)
+static cudaError_t pick(Params& p, int dt, int out_dt, bool vec, cudaStream_t s)
 {
     auto by_out = [&](auto d) {
         constexpr int D = decltype(d)::value;
@@ -524,9 +534,6 @@ cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K,
     auto tiles = [&](uint32_t k) { return p.n_tiles * (uint32_t)((T + k - 1) / k); };
     if (tok == 256u && tiles(256u) < sms) tok = 128u;
     p.tiles = tiles(tok);
-    // split K in clusters while there are SMs for it and every CTA keeps a chunk
-    p.z = 1u;
-    while (tok <= 128u && p.z < 8u && p.tiles * p.z * 2u <= sms && p.chunks >= 2u * p.z) p.z *= 2u;
     if (!x_map(&p.map_x, x, dt, T, K, ldx, tok)) return cudaErrorInvalidValue;
     const bool vec = K % 64 == 0;                                  // (16-byte aligned codes, 4-byte aligned scales)
     if (tok == 32u) return pick<32>(p, dt, out_dt, vec, s);

@@ -118,6 +118,26 @@ def test_gemm_unaligned_rows_of_tall_products(orc, M, N, pad, dt):
     assert torch.all(dst[:, N:] == 9.0)
 
 
+@pytest.mark.parametrize("N,pad", [(2565, 0), (2560, 8), (2562, 1)])
+def test_gemm_unaligned_rows_of_many_tiles(orc, N, pad):
+    """As above with more tiles than SMs."""
+    rng = np.random.default_rng(N)
+    qa, ea = operand(rng, 2050, 96)
+    qb, eb = operand(rng, N, 96)
+    for dt in (torch.float32, torch.bfloat16):
+        dst = torch.full((2050, N + pad), 9.0, dtype=dt, device=G.DEV)
+        check(orc, qa, ea, qb, eb, dtypes=(dt,), out=dst[:, :N])
+        assert torch.all(dst[:, N:] == 9.0)
+
+
+@pytest.mark.parametrize("M,N", [(1, 100), (16, 2048), (100, 2500), (129, 700), (257, 1290), (513, 384)])
+@pytest.mark.parametrize("K", [512, 1056, 2560, 8224])
+def test_gemm_split_k(orc, M, N, K):
+    """Few tiles and long K: clusters of every size share a tile's K, with uneven parts."""
+    rng = np.random.default_rng(M + K)
+    check(orc, *operand(rng, M, K), *operand(rng, N, K))
+
+
 @pytest.mark.parametrize("M", [4, 260])
 def test_gemm_nan_scales_stay_in_their_rows(orc, M):
     rng = np.random.default_rng(4)

@@ -167,3 +167,26 @@ def test_linear_streams_and_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, w)
+
+
+def test_one_row_of_a_matrix_with_an_odd_pitch():
+    """The distance to a next row that is not there is no reason to refuse a call."""
+    gen = torch.Generator(device=G.DEV).manual_seed(3)
+    big = torch.randn((3, 133), generator=gen, device=G.DEV).to(torch.bfloat16)
+    q = torch.randint(0, 256, (40, 64), generator=gen, dtype=torch.uint8, device=G.DEV)
+    sc = torch.full((40, 8), 0x38, dtype=torch.uint8, device=G.DEV)
+    s2 = torch.ones(1, device=G.DEV)
+    assert torch.equal(nv4.linear_w4a16(big[:1, :128], q, sc, s2), nv4.linear_w4a16(big[:1, :128].clone(), q, sc, s2))
+    sm = nv4.mma_scales(torch.full((40, 4), 127, dtype=torch.uint8, device=G.DEV))
+    assert torch.equal(nv4.linear_mxfp4(big[:1, :128], q, sm), nv4.linear_mxfp4(big[:1, :128].clone(), q, sm))
+    with pytest.raises(nv4.NV4Error):
+        nv4.linear_w4a16(big[:2, :128], q, sc, s2)
+
+
+@pytest.mark.parametrize("T,N", [(17, 100), (20, 2048), (64, 2500), (128, 700), (129, 1290)])
+@pytest.mark.parametrize("K", [528, 1280, 2576, 8208])
+def test_linear_split_k(orc, T, N, K):
+    """Few tiles and long K: clusters of every size share a tile's K, with uneven parts."""
+    rng = np.random.default_rng(T + K)
+    q, sc = weights(rng, N, K)
+    check(orc, rows(rng, T, K, "bf16").to(G.DEV), q, sc, 0.0031, "bf16")
