@@ -483,7 +483,9 @@ NV4_API nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, con
  * NV4_FP32), then nv4_gemm_mxfp4 with the weights qw, sfw_mma [N, K].  The rules of both apply.
  * d_work: nv4_linear_mxfp4_work_bytes(M, K) bytes (0 up to 16 rows, which are quantized within the
  * product: d_work may be NULL then), 16-byte aligned, not shared by calls that may run at the same
- * time; nothing has to be in it and nothing is kept in it (NV4_ERR_LIMIT if work_bytes is less). */
+ * time; nothing has to be in it and nothing is kept in it (NV4_ERR_LIMIT if work_bytes is less).
+ * Up to 16 rows, layers of more than 2^25 weights run faster with a workspace of
+ * nv4_mxfp4_mma_scale_bytes(M, K) + M * K / 2 bytes; the result is the same. */
 NV4_API size_t nv4_linear_mxfp4_work_bytes(int64_t M, int64_t K);
 NV4_API nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, int64_t ldx,
                             const uint8_t* qw, const uint8_t* sfw_mma, int64_t N, nv4_dtype out_dt, void* out,

@@ -963,7 +963,8 @@ def nv4_linear_mxfp4_work_bytes(M: int, K: int) -> int:
 
 def nv4_linear_mxfp4(x, qw, sfw_mma, out, work=None, d_flags=None, stream=None):
     """out[M, N] = Q(x) @ W^T: x [M, K] (bf16 or float32) quantized to MXFP4, MXFP4 weights (codes
-    [N, K/2], scales in the MMA layout); work: nv4_linear_mxfp4_work_bytes(M, K) bytes (None if 0)."""
+    [N, K/2], scales in the MMA layout); work: nv4_linear_mxfp4_work_bytes(M, K) bytes (None if 0; with
+    up to 16 rows and more than 2^25 weights faster with nv4_mxfp4_mma_scale_bytes(M, K) + M K / 2)."""
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise NV4Error("x must be bf16 or float32")
     dev = _here(x, qw, sfw_mma, out, work, d_flags)
@@ -990,6 +991,8 @@ def linear_mxfp4(x, qw, sfw_mma, dtype=torch.bfloat16, d_flags=None, stream=None
     M, K = x.shape
     out = _new((M, qw.shape[0]), dtype, x, stream)
     n = nv4_linear_mxfp4_work_bytes(M, K)
+    if n == 0 and qw.shape[0] * K > 1 << 25:
+        n = nv4_mxfp4_mma_scale_bytes(M, K) + M * K // 2
     work = _new((n,), torch.uint8, x, stream) if n else None
     nv4_linear_mxfp4(x, qw, sfw_mma, out, work, d_flags, stream)
     return out

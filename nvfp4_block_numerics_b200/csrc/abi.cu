@@ -559,11 +559,16 @@ nv4_status nv4_gemm_mxfp4(const uint8_t* qa, const uint8_t* sfa_mma, const uint8
                                        (cudaStream_t)stream));
 }
 
+// x as codes and scales in the MMA layout; 0 for sizes that are refused.
+static size_t quantized_bytes(int64_t M, int64_t K)
+{
+    const size_t sf = nv4_mxfp4_mma_scale_bytes(M, K);
+    return sf == 0 ? 0 : sf + (size_t)M * (size_t)(K / 2);
+}
+
 size_t nv4_linear_mxfp4_work_bytes(int64_t M, int64_t K)
 {
-    if (M <= kMaxFusedRows) return 0;
-    const size_t sf = nv4_mxfp4_mma_scale_bytes(M, K);             // 0 for sizes that are refused
-    return sf == 0 ? 0 : sf + (size_t)M * (size_t)(K / 2);
+    return M <= kMaxFusedRows ? 0 : quantized_bytes(M, K);
 }
 
 nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
@@ -571,7 +576,8 @@ nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int64_t K, i
                             size_t work_bytes, uint32_t* d_flags, void* stream)
 {
     if (dt != NV4_BF16 && dt != NV4_FP32) return NV4_ERR_DTYPE;
-    if (M > kMaxFusedRows) {
+    const bool wide = M > 0 && N > 0 && K > 0 && N > kMaxFusedWeights / K && d_work != nullptr && work_bytes >= quantized_bytes(M, K);
+    if (M > kMaxFusedRows || wide) {
         uint8_t* sf = static_cast<uint8_t*>(d_work);               // a multiple of 512 bytes
         uint8_t* q = sf == nullptr ? nullptr : sf + nv4_mxfp4_mma_scale_bytes(M, K);
         if (N > 0 && K > 0 && K % 32 == 0 && d_work != nullptr && work_bytes < nv4_linear_mxfp4_work_bytes(M, K))

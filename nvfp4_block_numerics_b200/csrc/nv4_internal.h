@@ -132,11 +132,16 @@ cudaError_t launch_gemm_mxfp4_small(const uint8_t* qa, const uint8_t* sfa, const
 // Rows of A up to which launch_gemm_mxfp4 runs on launch_gemm_mxfp4_small (and above them while its
 // 128 x 128 tiles fit the SMs at once), else on the CTA-pair kernel.  Either, in us: 128 x 2880 x 2880
 // 8.5 / 15.7, 128 x 16384 x 2048 10.2 / 11.6, 128 x 8192 x 8192 14.9 / 25.9, 256 x 2048 x 16384 14.6 /
-// 45, 1024 x 2048 x 2048 10.0 / 11.4.
-constexpr int64_t kMaxSmallRows = 128;
+// 45, 1024 x 2048 x 2048 10.0 / 11.4; with more tiles than SMs 64 x 32768 x 4096 22.2 / 26.2, 64 x 65536
+// x 4096 47.4 / 46.8, 128 x 65536 x 4096 55.0 / 48.2, 128 x 151936 x 1024 68 / 37.
+constexpr int64_t kMaxSmallRows = 64;
 // The linear layer for up to kMaxFusedRows rows: quantization and product in one kernel.  On the
 // device it is level with two (16 x 16384 x 2048 9.3 us, 16 x 2880 x 2880 7.0); a call costs one launch
-// less (1 x 2880 x 2880: 12.5 us a call, 17.5 with two).
+// less (1 x 2880 x 2880: 12.5 us a call, 17.5 with two).  Every tile quantizes the rows again, so past
+// kMaxFusedWeights weights two kernels are faster, if there is a workspace for them (16 rows, fused / the
+// product alone, to which the quantizer adds 3 us: 20000 x 512 8.5 / 7.3, 32768 x 1024 11.1 / 9.3, 8192 x
+// 8192 15.5 / 11.0, 32768 x 4096 29.5 / 19.0, 65536 x 4096 64 / 41).
+constexpr int64_t kMaxFusedWeights = (int64_t)1 << 25;
 constexpr int64_t kMaxFusedRows = 16;
 cudaError_t launch_linear_mxfp4_small(const void* x, int in_dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
                                       const uint8_t* sfw, int64_t N, int out_dt, void* out, int64_t ldd, uint32_t* d_flags,

@@ -222,3 +222,24 @@ def test_linear_quantizes_within_the_product(orc, dt, M, N, K):
     f = G.flags_dev()
     y = nv4.linear_mxfp4(xs, dq, ds, torch.float32, f)
     assert f.item() == nv4.FLAG_NONFINITE and torch.isnan(y[M - 1]).all() and torch.isfinite(y[:M - 1]).all()
+
+
+@pytest.mark.parametrize("M", [1, 16])
+def test_linear_mxfp4_of_a_wide_layer(orc, M):
+    """More than 2^25 weights: quantized within the product without a workspace, in front of it with
+    one; the same bits either way, and the oracle's values."""
+    rng = np.random.default_rng(8)
+    N, K = 34000, 992
+    qw, ew = operand(rng, N, K)
+    dq, ds = G.u8_dev(qw), nv4.mma_scales(G.u8_dev(ew))
+    x = torch.from_numpy(rng.laplace(size=(M, K)).astype(np.float32)).to(G.DEV)
+    without = torch.empty((M, N), dtype=torch.float32, device=G.DEV)
+    nv4.nv4_linear_mxfp4(x, dq, ds, without)
+    y = nv4.linear_mxfp4(x, dq, ds, dtype=torch.float32)
+    assert torch.equal(y, without)
+    q, e, _ = orc.mxfp4_quant(x.cpu().numpy())
+    D, Dabs = orc.gemm_mxfp4(q, e, qw, ew)
+    tol = (K / 64 + 4) * 2.0 ** -23 * Dabs + 2.0 ** -24 * np.abs(D) + 1e-38
+    assert np.all(np.abs(y.double().cpu().numpy() - D) <= tol)
+    with pytest.raises(nv4.NV4Error):
+        nv4.nv4_linear_mxfp4(x, dq, ds, without, torch.empty(1 << 17, dtype=torch.uint8, device=G.DEV)[8:])
