@@ -595,6 +595,7 @@ gemm_pair_kernel(const __grid_constant__ Params p)
             if constexpr (kOut == 2) {
 #pragma unroll 1
                 for (int cb = 0; cb < 4; ++cb) {
+                    if (kMx && col0 + 32 * cb >= p.N) break;       // the warp's columns are the same
                     float v[32];
                     tmem_ld32(taddr + (uint32_t)(32 * cb), v);
                     if (kMx && (p.vec == 0u || col0 + 32 * cb + 32 > p.N)) {
@@ -642,6 +643,7 @@ gemm_pair_kernel(const __grid_constant__ Params p)
                 const int pr = lane >> 1, pc = lane & 1;
 #pragma unroll
                 for (int c16 = 0; c16 < 8; ++c16) {
+                    if (kMx && col0 + 16 * c16 >= p.N) break;
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         *reinterpret_cast<uint4*>(st + 32 * lane + 16 * (k ^ ((lane >> 2) & 1))) =
