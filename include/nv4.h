@@ -470,7 +470,8 @@ NV4_API nv4_status nv4_hadamard2_nvfp4_quant(const void* w, nv4_dtype dt, int64_
  * e2m1 * 2^(e8m0 - 127).  Products are exact, accumulation is FP32 on the tensor cores; out
  * (NV4_BF16 or NV4_FP32, [M, N], leading dimension ldd >= N, 16-byte aligned base) is rounded
  * once.  M and N are any, K a multiple of 32.  A scale code 0xFF (NaN) makes its row's (A) or
- * column's (B) outputs NaN.  M == 0 or N == 0 is a no-op.
+ * column's (B) outputs NaN; so does one in the layout's padding behind the row's last block (both
+ * writers of the layout put zeros there).  M == 0 or N == 0 is a no-op.
  */
 NV4_API size_t nv4_mxfp4_mma_scale_bytes(int64_t rows, int64_t cols);
 NV4_API nv4_status nv4_mxfp4_quant_mma(const void* x, nv4_dtype dt, int64_t rows, int64_t cols, int64_t ld,

@@ -613,7 +613,7 @@ nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, i
     if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned16(out) || ldx % 8 != 0) return NV4_ERR_ALIGN;
     if (K > kMaxW4K || T >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || ((T + 31) / 32) * ((N + 127) / 128) >= (int64_t)1 << 31)
         return NV4_ERR_LIMIT;
-    if (T > kMaxFewRows)
+    if (!few_rows_w4a16(T, K))
         return from_cuda(launch_linear_w4a16_mma(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd, d_flags,
                                                  (cudaStream_t)stream));
     return from_cuda(launch_linear_w4a16(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd,

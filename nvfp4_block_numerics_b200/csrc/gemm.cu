@@ -24,8 +24,8 @@
 //     instruction stream (8192^3: 2.85 -> 4.03 PFLOP/s; the copies cost per instruction,
 //     not per byte).
 //   * warp 9: allocates the tensor memory (the 128 x kBN FP32 accumulator and the scale
-//     buffers); one lane waits until the epilogue has read the previous tile's accumulator
-//     ("acc_empty"), then per stage waits for the codes and the scales and issues four
+//     buffers); all its lanes wait until the epilogue has read the previous tile's accumulator
+//     ("acc_empty") and per stage for the codes and the scales; an elected one issues four
 //     tcgen05.mma kind::mxf4nvf4 block16 (K = 64 each) with both operands read from shared
 //     memory through matrix descriptors, commits "empty" and "sf_free", and commits
 //     "acc_full" after the tile's last stage.
@@ -43,6 +43,8 @@
 // gemm_pair_kernel below: 256 x 256 tiles, the 2-SM MMA): 8192^3 +2%, 16384 x 16384 x
 // 2048 +7%.  Its cross-CTA hand-offs use plain (CTA-scope) mbarrier waits and remote
 // arrives: with cluster-scope acquire/release on them the same kernel ran 40% slower.
+// The pair kernel also multiplies MXFP4 operands (kMx: kind::mxf4 block32, E8M0 scales, any M and N; 16384
+// x 16384 x 2048 in 325 us, 3.4 PFLOP/s); products of few rows or few tiles are gemm_mx.cu's.
 // Every mbarrier wait is bounded (kWaitLimitNs); on expiry the kernel sets
 // NV4_FLAG_TIMEOUT, every role stops, the stores are skipped, copies in flight are
 // drained and the tensor memory is released.

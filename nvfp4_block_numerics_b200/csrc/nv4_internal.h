@@ -93,6 +93,10 @@ constexpr size_t kMaxSmemW4 = 220u * 1024u;
 // form.  16 rows on either (us): 2880 x 2880 8.8 / 9.9, 16384 x 2048 11.1 / 15.3, 8192 x 8192 23.4 /
 // 27.5; a third column of 8 tokens would cost the former what the latter's 32 columns have free.
 constexpr int64_t kMaxFewRows = 16;
+// Whether a call runs on launch_linear_w4a16: few rows, and shared memory holds them (5 rows of 65536, 8
+// of 32768; read in passes instead, each of which reads the weights again, 16 x 8192 x 65536 took 605 us,
+// against 170; layers of a few hundred rows lose by it, 16 x 300 x 65536 37 us, against 48).
+bool few_rows_w4a16(int64_t T, int64_t K);
 cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
                                 cudaStream_t s);

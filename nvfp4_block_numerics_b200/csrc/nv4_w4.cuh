@@ -19,9 +19,9 @@
 // deliver.  The same through BF16 (mask and shift, bf16x2 multiply) gives 9.4 T/s, below it.
 // So the token rows are FP16 too.  FP16 rows are taken as they are.  BF16 rows are multiplied by
 // 2^4 and converted, exact for magnitudes from 2^-21 to 2^12 (8 significant bits above the last
-// FP16 bit, 2^-24).  If a pass holds others, its rows are read again, each with a power of two of
+// FP16 bit, 2^-24).  If a call has others, its rows are read again, each with a power of two of
 // its own (largest exponent to 2^14): exact for elements down to 2^-31 of the row's largest.  If
-// a row spans more, or holds a NaN, an Inf or a BF16 subnormal, the pass uses BF16 operands
+// a row spans more, or holds a NaN, an Inf or a BF16 subnormal, the call uses BF16 operands
 // (kWide: the same codes, converted once more), which is exact for every input.
 #pragma once
 
@@ -292,7 +292,7 @@ __device__ __forceinline__ uint32_t vec_offset(uint32_t v)
 __host__ __device__ inline uint32_t padded(uint32_t K) { return (K + kChunk - 1u) / kChunk * kChunk; }
 
 // ---------------------------------------------------------------- token rows into shared memory
-// Per token of a pass: exponent statistics and the factor that undoes its scaling.
+// Per token: exponent statistics and the factor that undoes its scaling.
 struct Rows {
     uint32_t emax[kMaxFewRows], emin[kMaxFewRows];          // largest / smallest non-zero BF16 magnitude bits
     float descale[kMaxFewRows];
@@ -313,7 +313,7 @@ __device__ __forceinline__ uint32_t vec_at(uint32_t c, uint32_t l, uint32_t m, u
 
 // Converts m token rows (row(i): pointer to K values of the input type, 16-byte aligned) into
 // xs, [chunk][8][m][4] vectors, zero-padded to whole chunks.  kDt 0: BF16, 1: FP16.  Returns
-// (to every thread) whether the pass has to use BF16 operands.  All threads take part; ends
+// (to every thread) whether the product has to use BF16 operands.  All threads take part; ends
 // with a CTA barrier.  A warp takes one chunk of one token at a time.
 template <int kDt, class RowPtr>
 __device__ __forceinline__ bool stage_tokens(uint4* xs, Rows& rows, uint32_t m, uint32_t K, RowPtr row)
