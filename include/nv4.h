@@ -527,9 +527,9 @@ NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int6
  * nv4_moe_experts -- out[t, :] = sum_j weights[t, j] * down_e ( silu(gate_e x_t) * (up_e x_t) ),
  * e = ids[t, j], silu(z) = z / (1 + exp(-z)).  An id outside [0, E) is no expert and adds
  * nothing (padded rows: out is 0 if a token has none); an id that a token names more than once
- * counts with the sum of its weights.  The hidden values are FP32, rounded to FP16 relative to
- * their row's largest magnitude for the down product; all sums are FP32; results do not depend
- * on the order in which CTAs run.
+ * counts with the sum of its weights.  The hidden values are FP32; the down product takes them as
+ * two FP16 parts, 22 bits (a relative error of 2^-22, or 2^-50 of their row's largest magnitude);
+ * all sums are FP32; results do not depend on the order in which CTAs run.
  *
  * nv4_moe_layer -- both, one after the other.
  *

@@ -18,7 +18,8 @@
 //     MMA row groups of 8 gate rows and the same 8 up rows, so both halves of an h meet in one
 //     thread.  h goes to the workspace in FP32.
 //   * moe_hidden_kernel, one CTA per (expert, token) row of h: scales it by a power of two and
-//     rounds it to FP16 (11 bits: a relative error of 2^-11, an eighth of the BF16 output's own).
+//     writes it as two FP16 values, h = hi + 2^-11 lo: 22 bits, a relative error of 2^-22 (one FP16
+//     value, 2^-11, was a visible part of the outputs' error).
 //   * moe_down_kernel, one CTA per SM: a CTA owns a range of output rows for all tokens and all
 //     chosen experts, so the sum over a token's experts needs no other CTA and is in a fixed
 //     order.  The row's scale, the expert's scale_2 and the routing weight are applied in FP32.
@@ -46,8 +47,8 @@ constexpr uint32_t kPass = 8;                     // tokens of one expert multip
 
 // ---------------------------------------------------------------- token rows
 // The workspace: x as FP16 in vector order [T][H padded], what undoes each row's scaling
-// (negative: the row is not held by FP16, see w4::stage_tokens), h in FP32 [rows][I], h as FP16 in
-// vector order [rows][I padded], its scales.
+// (negative: the row is not held by FP16, see w4::stage_tokens), h in FP32 [rows][I], h in two FP16
+// parts in vector order [rows][2][I padded], its scales.
 struct Work {
     uint16_t* x16;
     float* xd;
@@ -71,7 +72,7 @@ __host__ inline Work work_of(void* w, size_t T, size_t k, size_t H, size_t I, si
     o.x16 = reinterpret_cast<uint16_t*>(take(T * w4::padded((uint32_t)H) * 2u));
     o.xd = reinterpret_cast<float*>(take(T * 4u));
     o.h = reinterpret_cast<float*>(take(T * k * I * 4u));
-    o.h16 = reinterpret_cast<uint16_t*>(take(T * k * w4::padded((uint32_t)I) * 2u));
+    o.h16 = reinterpret_cast<uint16_t*>(take(T * k * w4::padded((uint32_t)I) * 4u));
     o.hd = reinterpret_cast<float*>(take(T * k * 4u));
     *bytes = at;
     return o;
@@ -499,8 +500,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     }
 }
 
-// ---------------------------------------------------------------- h to FP16
-// One CTA per row (rows that no pair has are converted too, and read by nothing).
+// ---------------------------------------------------------------- h to two FP16 parts
+// One CTA per row (rows that no pair has are converted too, and read by nothing).  What hi leaves of
+// a value is at most 2^-11 of it (and exact in FP32): lo, 2^11 times that, is within FP16's range
+// again and rounds it by 2^-22 of the value, or by 2^-50 of the row's largest.  Nothing is left of an
+// Inf or a NaN.
 __global__ void __launch_bounds__(256) moe_hidden_kernel(const __grid_constant__ Experts p)
 {
     __shared__ uint32_t red[8];
@@ -547,11 +551,19 @@ __global__ void __launch_bounds__(256) moe_hidden_kernel(const __grid_constant__
     if (tid == 0u) p.work.hd[blockIdx.x] = w4::exp_field(254 - fe);
     auto put = [&](uint32_t v, const float4& a, const float4& b) {
         const float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t o[4];
+        uint32_t o[4], l[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(__fmul_rn(z[2 * j + 1], f)), "f"(__fmul_rn(z[2 * j], f)));
-        *reinterpret_cast<uint4*>(p.work.h16 + (size_t)blockIdx.x * w4::padded(p.I) + w4::vec_offset(v)) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; ++j) {
+            float s[2] = {__fmul_rn(z[2 * j], f), __fmul_rn(z[2 * j + 1], f)}, h[2];
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(s[1]), "f"(s[0]));
+            f16x2_to_f32(o[j], h[0], h[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[i] = fabsf(h[i]) <= FLT_MAX ? (s[i] - h[i]) * 0x1p11f : 0.0f;
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(l[j]) : "f"(s[1]), "f"(s[0]));
+        }
+        uint16_t* at = p.work.h16 + 2u * (size_t)blockIdx.x * w4::padded(p.I) + w4::vec_offset(v);
+        *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(at + w4::padded(p.I)) = make_uint4(l[0], l[1], l[2], l[3]);
     };
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
@@ -599,15 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     const uint32_t steps = works ? (uint32_t)((uint64_t)(widx + 1u) * n / wpt) - s0 : 0u;
     uint32_t us = s0 / nch, uc = s0 - us * nch, ua = steps != 0u ? L.find(us) : 0u;
     uint32_t ls = us, lc = uc, la = ua;
-    w4::Rows16 rw;
+    size_t row = 0u;                                               // byte offset of this lane's codes (scales: an eighth)
     bool moved = true;
     auto load = [&](uint8_t* slot) {
         if (moved) {
             if (ls >= L.sub[la + 1u]) ++la;
-            const size_t row = ((size_t)L.expert[la] * p.H + r0 + ta + g) * (p.I / 2u), row8 = row + (size_t)8u * (p.I / 2u);
-            rw.set(p.dq + row, p.ds + row / 8u, p.dq + row8, p.ds + row8 / 8u, g < tn, g + 8u < tn);
+            row = ((size_t)L.expert[la] * p.H + r0 + ta + g) * (p.I / 2u);
             moved = false;
         }
+        const uint32_t eight = 8u * (p.I / 2u);
+        w4::Rows16 rw;
+        rw.set(p.dq + row, p.ds + row / 8u, p.dq + row + eight, p.ds + row / 8u + eight / 8u, g < tn, g + 8u < tn);
         w4::load_chunk<kVec>(slot, rw, lc, p.I);
         if (++lc == nch) {
             lc = 0u;
@@ -621,35 +635,58 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     __syncthreads();                                               // coef
     for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) coef[i] *= p.work.hd[i];
     __syncthreads();
-    w4::Acc<1> acc[1];
-    w4::clear<1>(acc[0]);
+    w4::AccOf<2, 2> acc;                                           // [chain][part of h]
+    w4::clear<2, 2>(acc);
+    const uint32_t part = w4::padded(p.I);
     uint32_t left = steps, f0 = 0u, m = 0u;
     const uint16_t* xr = nullptr;
-    bool fresh = true;
+    bool fresh = true, paired = false;
     ring.run(load, [&](const uint8_t* slot) {
         if (fresh) {
             if (us >= L.sub[ua + 1u]) ++ua;
             f0 = L.first[ua] + (us - L.sub[ua]) * kPass;
             m = min(kPass, L.first[ua + 1u] - f0);
-            xr = p.work.h16 + (size_t)(f0 + min(g, m - 1u)) * w4::padded(p.I);
+            // up to 4 rows: both parts of a row are columns of one MMA, 4 apart
+            paired = m <= 4u;
+            const uint32_t col = paired ? g & 3u : g;
+            xr = p.work.h16 + 2u * (size_t)(f0 + min(col, m - 1u)) * part + (paired && g >= 4u ? part : 0u);
             fresh = false;
         }
-        w4::mma_rows<false, 1, 4>(acc, slot, xr, uc, p.I);
+        if (paired) {
+            w4::mma_rows<false, 1, 4>(reinterpret_cast<w4::AccOf<1, 4>(&)[1]>(acc), slot, xr, uc, p.I);
+        } else {
+            const uint16_t* at = xr + uc * kChunk + 8u * t;
+#pragma unroll 1                                                   // (what a launch pays for fetching the code counts)
+            for (uint32_t q = 0; q < 2; ++q, at += 128u) {
+                uint4 x[2][4];
+#pragma unroll
+                for (uint32_t j = 0; j < 2; ++j)
+#pragma unroll
+                    for (uint32_t u = 0; u < 4; ++u) x[j][u] = *reinterpret_cast<const uint4*>(at + j * part + 32u * u);
+                w4::mma_half<false, 2, 2>(acc, slot, q, [&](uint32_t j, uint32_t u) { return x[j][u & 3u]; });
+            }
+        }
         --left;
         if (++uc < nch && left != 0u) return;
         // the sub-list's end: its columns, each times its coefficient, into the warp's sums
-        w4::join<1>(acc[0]);
+        float v[4];                                                // rows g (columns 2 t, 2 t + 1) and g + 8
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            const float a = acc[0][0][i] + acc[1][0][i], b = acc[0][1][i] + acc[1][1][i];
+            const float lo = __shfl_xor_sync(0xFFFFFFFFu, a + b, 2);           // paired: four chains of columns 4 - 7
+            v[i] = paired ? a + b + lo * 0x1p-11f : a + b * 0x1p-11f;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < 2; ++i) {
             const uint32_t col = 2u * t + i;
             if (col < m) {
                 float* y = Y + (size_t)L.tok[f0 + col] * 16u;
-                y[g] += acc[0][0][0][i] * coef[f0 + col];
-                y[g + 8] += acc[0][0][0][2 + i] * coef[f0 + col];
+                y[g] += v[i] * coef[f0 + col];
+                y[g + 8] += v[2 + i] * coef[f0 + col];
             }
         }
         __syncwarp();
-        w4::clear<1>(acc[0]);
+        w4::clear<2, 2>(acc);
         uc = 0u;
         ++us;
         fresh = true;

@@ -206,42 +206,46 @@ using AccOf = float[kCh][NT][4];
 template <int NT>
 using Acc = float[kChains<NT>][NT][4];
 
-// acc += 16 weight rows x token rows over one chunk.  x(j, u): this lane's 16-byte vector of token
-// 8 j + g, the 8 elements from 128 (u / 4) + 32 t + 8 (u % 4) of the chunk on.
+// acc += 16 weight rows x token rows over half p of one chunk.  x(j, u): this lane's 16-byte vector of
+// token 8 j + g, the 8 elements from 128 (u / 4) + 32 t + 8 (u % 4) of the chunk on.
+template <bool kWide, int NT, int kCh, class X>
+__device__ __forceinline__ void mma_half(AccOf<NT, kCh>& acc, const uint8_t* slot, uint32_t p, X x)
+{
+    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+    const uint4 qa = *reinterpret_cast<const uint4*>(slot + 512u * p + 16u * lane);
+    const uint4 qb = *reinterpret_cast<const uint4*>(slot + 1024u + 512u * p + 16u * lane);
+    uint32_t s0[2], s1[2];
+    scale_pair(*reinterpret_cast<const uint16_t*>(slot + 2048u + 16u * g + 8u * p + 2u * t), s0);
+    scale_pair(*reinterpret_cast<const uint16_t*>(slot + 2048u + 128u + 16u * g + 8u * p + 2u * t), s1);
+    const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u) {
+        uint32_t a[4], b[4];
+        cvt_e2m1x8_to_f16x8(wa[u], a);
+        cvt_e2m1x8_to_f16x8(wb[u], b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = mul_f16x2(a[i], s0[u >> 1]);
+            b[i] = mul_f16x2(b[i], s1[u >> 1]);
+            if constexpr (kWide) {
+                a[i] = f16x2_to_bf16x2(a[i]);
+                b[i] = f16x2_to_bf16x2(b[i]);
+            }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < (uint32_t)NT; ++j) {
+            const uint4 v = x(j, 4u * p + u);
+            mma<kWide>(acc[(2u * u) % kCh][j], a[0], b[0], a[1], b[1], v.x, v.y);
+            mma<kWide>(acc[(2u * u + 1u) % kCh][j], a[2], b[2], a[3], b[3], v.z, v.w);
+        }
+    }
+}
+
 template <bool kWide, int NT, int kCh, class X>
 __device__ __forceinline__ void mma_step(AccOf<NT, kCh>& acc, const uint8_t* slot, X x)
 {
-    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
 #pragma unroll
-    for (uint32_t p = 0; p < 2; ++p) {
-        const uint4 qa = *reinterpret_cast<const uint4*>(slot + 512u * p + 16u * lane);
-        const uint4 qb = *reinterpret_cast<const uint4*>(slot + 1024u + 512u * p + 16u * lane);
-        uint32_t s0[2], s1[2];
-        scale_pair(*reinterpret_cast<const uint16_t*>(slot + 2048u + 16u * g + 8u * p + 2u * t), s0);
-        scale_pair(*reinterpret_cast<const uint16_t*>(slot + 2048u + 128u + 16u * g + 8u * p + 2u * t), s1);
-        const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
-#pragma unroll
-        for (uint32_t u = 0; u < 4; ++u) {
-            uint32_t a[4], b[4];
-            cvt_e2m1x8_to_f16x8(wa[u], a);
-            cvt_e2m1x8_to_f16x8(wb[u], b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = mul_f16x2(a[i], s0[u >> 1]);
-                b[i] = mul_f16x2(b[i], s1[u >> 1]);
-                if constexpr (kWide) {
-                    a[i] = f16x2_to_bf16x2(a[i]);
-                    b[i] = f16x2_to_bf16x2(b[i]);
-                }
-            }
-#pragma unroll
-            for (uint32_t j = 0; j < (uint32_t)NT; ++j) {
-                const uint4 v = x(j, 4u * p + u);
-                mma<kWide>(acc[(2u * u) % kCh][j], a[0], b[0], a[1], b[1], v.x, v.y);
-                mma<kWide>(acc[(2u * u + 1u) % kCh][j], a[2], b[2], a[3], b[3], v.z, v.w);
-            }
-        }
-    }
+    for (uint32_t p = 0; p < 2; ++p) mma_half<kWide, NT, kCh>(acc, slot, p, x);
 }
 
 // Token rows in shared memory, xs: the chunk's [8][m][4] vectors (u, token, t).  Columns past m
