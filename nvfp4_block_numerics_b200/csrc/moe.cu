@@ -579,8 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Lists L;
-    __shared__ float coef[kMaxMoePairs];                           // routing weight x expert scale x row scale
     float* Yall = reinterpret_cast<float*>(smem + w4::kRing);      // [16 warps][T][16]
+    // of a row of h: its scale, routing weight x expert scale (one product of the three, of a row near 2^-110
+    // say, could be subnormal where the result is not); as many as there are pairs, the rest of the SM is L1's
+    float2* coef = reinterpret_cast<float2*>(Yall + (size_t)kWarps * p.T * 16u);
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const uint32_t r0 = (uint32_t)((uint64_t)blockIdx.x * p.H / gridDim.x);
     const uint32_t R = (uint32_t)((uint64_t)(blockIdx.x + 1u) * p.H / gridDim.x) - r0;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             if (same && j < i) first = false;
             if (same) w += __ldcg(p.weights + j);
         }
-        if (first) coef[L.first[L.slot[e]] + __popcll(L.mask[e] & ((1ull << tok) - 1ull))] = w * __ldg(p.d2 + e);
+        if (first) coef[L.first[L.slot[e]] + __popcll(L.mask[e] & ((1ull << tok) - 1ull))].y = w * __ldg(p.d2 + e);
     }
     // this warp's run of the tile's (sub-list, chunk) steps
     const uint32_t n = L.subs * nch, s0 = works ? (uint32_t)((uint64_t)widx * n / wpt) : 0u;
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     ring.begin(smem + warp * (w4::kDepth * w4::kSlot), steps, load);
     w4::pdl_wait();                                                // h is complete
     __syncthreads();                                               // coef
-    for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) coef[i] *= p.work.hd[i];
+    for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) coef[i].x = p.work.hd[i];
     __syncthreads();
     w4::AccOf<2, 2> acc;                                           // [chain][part of h]
     w4::clear<2, 2>(acc);
@@ -681,8 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             const uint32_t col = 2u * t + i;
             if (col < m) {
                 float* y = Y + (size_t)L.tok[f0 + col] * 16u;
-                y[g] += v[i] * coef[f0 + col];
-                y[g + 8] += v[2 + i] * coef[f0 + col];
+                const float2 c = coef[f0 + col];
+                y[g] += v[i] * c.x * c.y;
+                y[g + 8] += v[2 + i] * c.x * c.y;
             }
         }
         __syncwarp();
@@ -768,11 +771,10 @@ static cudaError_t run_down(const Experts& p, cudaStream_t s)
     static bool ready[64] = {};
     const uint32_t sms = (uint32_t)num_sms(), grid = p.H < sms ? p.H : sms;
     if ((p.H + grid - 1u) / grid > 16u * kWarps) return cudaErrorInvalidValue;
-    constexpr uint32_t most = kWarps * (uint32_t)kMaxMoeTokens * 16u * (uint32_t)sizeof(float);
-    const cudaError_t e = prepare(moe_down_kernel<kOut, kVec>, ready, (int)(w4::kRing + most), false);
+    auto smem = [](size_t T, size_t pairs) { return w4::kRing + kWarps * T * 16u * sizeof(float) + pairs * sizeof(float2); };
+    const cudaError_t e = prepare(moe_down_kernel<kOut, kVec>, ready, (int)smem((size_t)kMaxMoeTokens, (size_t)kMaxMoePairs), false);
     if (e != cudaSuccess) return e;
-    return launch(moe_down_kernel<kOut, kVec>, p, grid, kThreads, w4::kRing + kWarps * (size_t)p.T * 16u * sizeof(float), 1u, true,
-                  s);
+    return launch(moe_down_kernel<kOut, kVec>, p, grid, kThreads, smem(p.T, (size_t)p.T * p.k), 1u, true, s);
 }
 
 }  // namespace moe

@@ -76,3 +76,26 @@ def test_hidden_values_keep_their_bits(dt, T, E, H, I):
                         G.f32_dev(w.astype(np.float32)), g, u, d, dtype=torch.float32)
     want = expected(x, ids, w, vals) / 8.0
     assert np.array_equal(y.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("T", [2, 7])
+@pytest.mark.parametrize("s_up,s_down", [(-80, -55), (80, 40), (-60, 30), (0, 0)])
+def test_scales_far_from_one(T, s_up, s_down):
+    """Hidden values and scale_2 of extreme magnitudes whose product is an ordinary number: the sum is exact, the
+    routing weight times scale_2 is exact (0.7 times a power of two), so one rounding is left, 2^-24, or 2^-150 where the
+    result is subnormal; from 2^128 on the result is an Inf.  (I is one chunk of 256: one warp forms the whole sum.)"""
+    rng = np.random.default_rng(T)
+    E, H, I = 2, 64, 240
+    codes, vals = whole_number_layer(rng, E, H, I)
+    x = tokens(rng, T, H)
+    ids = rng.integers(0, E, (T, 1))
+    w = np.float32(0.7)
+    g, u, d = dev(codes[0], 1.0), dev(codes[1], 2.0 ** s_up), dev(codes[2], 2.0 ** s_down)
+    y = nv4.moe_experts(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).to(G.DEV),
+                        torch.from_numpy(ids.astype(np.int32)).to(G.DEV), torch.full((T, 1), 0.7, device=G.DEV), g, u, d,
+                        dtype=torch.float32).double().cpu().numpy()
+    want = expected(x, ids, np.ones((T, 1), np.int64), vals) / 8.0 * float(w) * 2.0 ** (s_up + s_down)
+    big = np.abs(want) >= 2.0 ** 128
+    assert np.array_equal(y[big], np.copysign(np.inf, want[big]))
+    y, want = y[~big], want[~big]
+    assert np.all(np.abs(y - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -150)
