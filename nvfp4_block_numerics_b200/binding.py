@@ -746,7 +746,11 @@ def _new(shape, dtype, x: torch.Tensor, stream) -> torch.Tensor:
     """An output allocated for the stream that the call runs on."""
     if stream is None:
         return x.new_empty(shape, dtype=dtype)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=x.device)
+    if isinstance(stream, torch.cuda.Stream):
+        s = stream
+    else:
+        h = _stream(stream)                       # (an ExternalStream of handle 0 would be some stream of torch's pool)
+        s = torch.cuda.ExternalStream(h, device=x.device) if h else torch.cuda.default_stream(x.device)
     with torch.cuda.stream(s):
         return x.new_empty(shape, dtype=dtype)
 
