@@ -471,7 +471,8 @@ NV4_API nv4_status nv4_hadamard2_nvfp4_quant(const void* w, nv4_dtype dt, int64_
  * (NV4_BF16 or NV4_FP32, [M, N], leading dimension ldd >= N, 16-byte aligned base) is rounded
  * once.  M and N are any, K a multiple of 32.  A scale code 0xFF (NaN) makes its row's (A) or
  * column's (B) outputs NaN; so does one in the layout's padding behind the row's last block (both
- * writers of the layout put zeros there).  M == 0 or N == 0 is a no-op.
+ * writers of the layout put zeros there); *d_flags does not report it.  M == 0 or N == 0 is a no-op.
+ * NV4_FLAG_TIMEOUT: some output tiles were not stored.
  */
 NV4_API size_t nv4_mxfp4_mma_scale_bytes(int64_t rows, int64_t cols);
 NV4_API nv4_status nv4_mxfp4_quant_mma(const void* x, nv4_dtype dt, int64_t rows, int64_t cols, int64_t ld,
@@ -507,7 +508,8 @@ NV4_API nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int6
  * T is any number of rows (one decoded token to a prompt), N any, K a multiple of 16 (and
  * K <= 65536, NV4_ERR_LIMIT beyond).  e2m1 * e4m3 is exact in the product's operands, sums are
  * FP32, the result is rounded once to out_dt.  A NaN or Inf in x or a NaN scale propagates to
- * the outputs that it reaches.  T == 0 or N == 0 is a no-op.
+ * the outputs that it reaches.  T == 0 or N == 0 is a no-op.  NV4_FLAG_TIMEOUT: some output tiles
+ * were not stored.
  */
 NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, int64_t ldx,
                             const uint8_t* q, const uint8_t* scales, const float* d_s2, int64_t N,
@@ -596,6 +598,15 @@ NV4_API nv4_status nv4_fp32_probe(int packed, uint32_t blocks, uint32_t iters, f
  * Not a paper operation: the failure-detection path, testable without any fault.
  */
 NV4_API nv4_status nv4_selftest_wait(const uint32_t* d_flag, uint64_t limit_ns, uint32_t* d_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * nv4_selftest_cluster -- exercises how the CTAs of a cluster that adds its partial sums learn that one
+ * of them gave up (nv4_linear_w4a16, nv4_gemm_mxfp4 and nv4_linear_mxfp4: none of them stores then).  CTA
+ * `rank` (0 to 7, or -1 for none; NV4_ERR_LIMIT beyond) of a cluster of eight says that it gave up;
+ * d_status[0..7]: NV4_FLAG_TIMEOUT for each CTA that saw it, else 0.  Nothing waits for it.
+ * Not a paper operation: the failure-detection path, testable without any fault.
+ */
+NV4_API nv4_status nv4_selftest_cluster(int rank, uint32_t* d_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -33,6 +33,7 @@ __all__ = [
     "nv4_linear_w4a16", "linear_w4a16", "nv4_moe_route", "nv4_moe_work_bytes", "nv4_moe_experts", "nv4_moe_layer",
     "moe_route", "moe_experts", "moe_layer", "ExpertWeights", "nv4_mxfp4_mma_scale_bytes", "nv4_mxfp4_quant_mma",
     "nv4_gemm_mxfp4", "nv4_linear_mxfp4", "nv4_linear_mxfp4_work_bytes", "mxfp4_quant_mma", "gemm_mxfp4", "linear_mxfp4",
+    "nv4_selftest_cluster",
 ]
 
 BF16, FP16, FP32 = 0, 1, 2
@@ -94,6 +95,7 @@ _SIGS = {
     "nv4_dequant": (C.c_int, [_vp, _vp, _vp, _i64, _i64, C.c_int, _vp, _vp]),
     "nv4_mma_scale_bytes": (C.c_size_t, [_i64, _i64]),
     "nv4_selftest_wait": (C.c_int, [_vp, C.c_uint64, _vp, _vp]),
+    "nv4_selftest_cluster": (C.c_int, [C.c_int, _vp, _vp]),
     "nv4_mxfp4_quant": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "nv4_mxfp4_dequant": (C.c_int, [_vp, _vp, _i64, _i64, C.c_int, _vp, _vp]),
     "nv4_fp8_quant": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
@@ -411,6 +413,12 @@ def nv4_selftest_wait(flag: torch.Tensor, limit_ns: int, status: torch.Tensor, s
     if flag.dtype != torch.int32 or status.dtype != torch.int32 or status.numel() < 2:
         raise NV4Error("flag and status must be int32 CUDA tensors (status of at least 2 elements)")
     _check(lib().nv4_selftest_wait(_ptr(flag), int(limit_ns), _ptr(status), _stream(stream)), "nv4_selftest_wait")
+
+
+def nv4_selftest_cluster(rank: int, status: torch.Tensor, stream=None):
+    if status.dtype != torch.int32 or status.numel() < 8 or not status.is_contiguous():
+        raise NV4Error("status must be a contiguous int32 CUDA tensor of at least 8 elements")
+    _check(lib().nv4_selftest_cluster(int(rank), _ptr(status), _stream(stream)), "nv4_selftest_cluster")
 
 
 def _w_rows(w, name="w"):

@@ -2,6 +2,7 @@
 // argument validation, then one stream-ordered kernel launch per call.
 #include <cstdint>
 
+#include "nv4_async.cuh"
 #include "nv4_common.cuh"
 #include "nv4_internal.h"
 
@@ -95,6 +96,25 @@ __global__ void wait_selftest_kernel(const volatile uint32_t* flag, uint64_t lim
 cudaError_t launch_wait_selftest(const uint32_t* flag, uint64_t limit_ns, uint32_t* status, cudaStream_t s)
 {
     wait_selftest_kernel<<<1, 32, 0, s>>>(flag, limit_ns, status);
+    return cudaGetLastError();
+}
+
+// What a cluster's CTAs learn of one that gave up, exercised alone: CTA `bad` of eight (none: any other
+// value) sets its word; status[i] = what CTA i sees.
+__global__ void __cluster_dims__(8, 1, 1) cluster_selftest_kernel(uint32_t bad, uint32_t* status)
+{
+    __shared__ uint32_t word;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0u) word = rank == bad ? 1u : 0u;
+    cluster_sync();
+    const bool any = cluster_any(&word, 8u);
+    cluster_sync();
+    if (threadIdx.x == 0u) status[rank] = any ? kFlagTimeout : 0u;
+}
+
+cudaError_t launch_cluster_selftest(uint32_t bad, uint32_t* status, cudaStream_t s)
+{
+    cluster_selftest_kernel<<<8, 32, 0, s>>>(bad, status);
     return cudaGetLastError();
 }
 
@@ -473,6 +493,13 @@ nv4_status nv4_selftest_wait(const uint32_t* d_flag, uint64_t limit_ns, uint32_t
     if (d_flag == nullptr || d_status == nullptr) return NV4_ERR_NULL;
     if (limit_ns > kWaitLimitNs) return NV4_ERR_LIMIT;
     return from_cuda(launch_wait_selftest(d_flag, limit_ns, d_status, (cudaStream_t)stream));
+}
+
+nv4_status nv4_selftest_cluster(int rank, uint32_t* d_status, void* stream)
+{
+    if (d_status == nullptr) return NV4_ERR_NULL;
+    if (rank < -1 || rank > 7) return NV4_ERR_LIMIT;
+    return from_cuda(launch_cluster_selftest((uint32_t)rank, d_status, (cudaStream_t)stream));
 }
 
 }  // extern "C"

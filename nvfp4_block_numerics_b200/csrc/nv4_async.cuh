@@ -121,4 +121,14 @@ __device__ __forceinline__ float ld_dsmem_f32(const float* local, uint32_t rank)
     return __uint_as_float(ld_dsmem_u32(local, rank));
 }
 
+// Whether the word at `local` is not zero in any of the cluster's z CTAs (between two cluster barriers).
+__device__ __forceinline__ bool cluster_any(const uint32_t* local, uint32_t z)
+{
+    uint32_t any = 0u;
+#pragma unroll
+    for (uint32_t k = 0; k < 8u; ++k)
+        if (k < z) any |= ld_dsmem_u32(local, k);
+    return any != 0u;
+}
+
 }  // namespace nv4

@@ -80,6 +80,7 @@ cudaError_t launch_hadamard2(int mode, const void* w, int dt, int64_t rows, int6
 cudaError_t launch_hadamard_quant(int mode, const void* x, int64_t rows, int64_t cols, int64_t ld, int n,
                                   float* d_amax, uint8_t* q, uint8_t* sc, float* d_s2, uint32_t* d_flags,
                                   cudaStream_t s);
+cudaError_t launch_cluster_selftest(uint32_t bad, uint32_t* status, cudaStream_t s);
 cudaError_t launch_wait_selftest(const uint32_t* flag, uint64_t limit_ns, uint32_t* status, cudaStream_t s);
 size_t mma_scale_bytes(int64_t rows, int64_t kb);
 cudaError_t launch_mma_scale_layout(const uint8_t* sc, int64_t rows, int64_t kb, uint8_t* out, cudaStream_t s);

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
             if (r >= rows) continue;
             const float4 sum = cluster_sum4(part + 4u * i, p.z);
             const float o[4] = {sum.x * s2, sum.y * s2, sum.z * s2, sum.w * s2};
-            if (aborted()) continue;
+            if (cluster_any(&sm.abort, p.z)) continue;             // a CTA that gave up has no sums to add
 #pragma unroll
             for (uint32_t k = 0; k < 4u; ++k)
                 if (r + k < rows) store1<kOut>(p.out, (int64_t)(tok0 + tok) * p.ldd + n0 + r + k, o[k]);
