@@ -522,9 +522,10 @@ NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int6
  * nv4_moe_route -- logits[t, e] = sum_h x[t, h] * w_router[e, h]; ids[t, 0..top_k) are the
  * experts with the largest logits in descending order, ties to the lower index; weights[t, j] =
  * softmax(logits[t])[ids[t, j]], divided by the sum of the chosen ones if renormalize != 0.
- * The logits are formed in FP64 (the products of 16-bit values are exact, so the choice does not
- * depend on the order of summation).  A NaN or Inf logit sets NV4_FLAG_NONFINITE; NaN ranks
- * last, and that token's weights are unspecified.
+ * The logits are formed in FP64: exact products over the whole range of dt, sums in a fixed order, each
+ * addition rounded to 53 bits.  Two logits closer than that rounding may come in either order (and two
+ * that would be equal, but are sums of different terms, may not tie).  A NaN or Inf logit sets
+ * NV4_FLAG_NONFINITE; NaN ranks last, and that token's weights are unspecified.
  *
  * nv4_moe_experts -- out[t, :] = sum_j weights[t, j] * down_e ( silu(gate_e x_t) * (up_e x_t) ),
  * e = ids[t, j], silu(z) = z / (1 + exp(-z)).  An id outside [0, E) is no expert and adds

@@ -9,10 +9,11 @@
 //
 // Four launches, each a programmatic dependent of the one before: its CTAs start, and do what
 // does not depend on it, while the last CTAs in front finish.
-//   * moe_route_kernel: a 16-CTA cluster per one or two tokens.  The products of 16-bit values
-//     are exact in FP32 (inside its range) and are summed in FP64, so that the choice of experts is
-//     that of the exact logits whatever the summation order.  It also converts BF16 token rows to FP16, each
-//     with a power of two of its own (moe_rows_kernel does where the experts are given).
+//   * moe_route_kernel: a 16-CTA cluster per one or two tokens.  The products are exact and are summed in
+//     FP64, so that the choice of experts is that of the exact logits unless two of them lie within the
+//     sums' rounding (2^-53 of the sum of magnitudes, per addition).  For BF16 that takes FP64 products (formed
+//     in FP32, which some leave, 48 tokens took 12.6 us instead of 16.2).  It also converts BF16 token rows to
+//     FP16, each with a power of two of its own (moe_rows_kernel does where the experts are given).
 //   * moe_up_kernel, one CTA per SM: the flat list (expert, i) of gate / up row pairs of the
 //     chosen experts is cut into one contiguous range per CTA, walked in tiles of 16 pairs, two
 //     MMA row groups of 8 gate rows and the same 8 up rows, so both halves of an h meet in one
@@ -204,7 +205,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
                     float v[8];
                     unpack8<kDt>(__ldg(reinterpret_cast<const uint4*>(x + (int64_t)i * p.ldx + h)), v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[i][j & 3] += (double)__fmul_rn(v[j], w[j]);   // exact product
+                    for (int j = 0; j < 8; ++j) {
+                        // exact products; those of FP16 fit FP32 (2^-48 to 2^32), with one conversion instead of two
+                        if constexpr (kDt == 0) s[i][j & 3] = fma((double)v[j], (double)w[j], s[i][j & 3]);
+                        else s[i][j & 3] += (double)__fmul_rn(v[j], w[j]);
+                    }
                 }
             }
         }
@@ -794,8 +799,8 @@ cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_
     RouteParams p{x, ldx, wr, ids, weights, (uint32_t)T, (uint32_t)H, (uint32_t)E, (uint32_t)top_k, (uint32_t)renorm, d_flags, {}};
     size_t n;
     if (then != nullptr) p.work = work_of(then->work, (size_t)T, (size_t)top_k, (size_t)H, (size_t)then->I, &n);
-    // a cluster per token while they all run at once (T = 8, 64 experts of 4096: 5.6 us, against 7.1
-    // with two tokens each), then two, which read the router's weights half as often (T = 48: 12.8)
+    // a cluster per token while they all run at once (T = 8, 64 experts of 4096: 6.1 us, against 7.3 for 9
+    // with two tokens each), then two, which read the router's weights half as often (T = 48: 16.2)
     if (T <= 8) return dt == 0 ? run_route<0, 1>(p, s) : run_route<1, 1>(p, s);
     return dt == 0 ? run_route<0, kRouteTokens>(p, s) : run_route<1, kRouteTokens>(p, s);
 }
