@@ -507,8 +507,8 @@ NV4_API nv4_status nv4_linear_mxfp4(const void* x, nv4_dtype dt, int64_t M, int6
  *          no rule for ldd.
  * T is any number of rows (one decoded token to a prompt), N any, K a multiple of 16 (and
  * K <= 65536, NV4_ERR_LIMIT beyond).  e2m1 * e4m3 is exact in the product's operands, sums are
- * FP32, the result is rounded once to out_dt.  A NaN or Inf in x or a NaN scale propagates to
- * the outputs that it reaches.  T == 0 or N == 0 is a no-op.  NV4_FLAG_TIMEOUT: some output tiles
+ * FP32, the result is rounded once to out_dt.  A NaN or Inf in x makes its row's outputs NaN or Inf, a
+ * NaN scale its column's; NV4_FLAG_NONFINITE is set if an output is NaN or Inf before that rounding.  T == 0 or N == 0 is a no-op.  NV4_FLAG_TIMEOUT: some output tiles
  * were not stored.
  */
 NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, int64_t ldx,

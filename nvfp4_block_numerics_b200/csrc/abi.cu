@@ -643,7 +643,7 @@ nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, i
     if (!few_rows_w4a16(T, K))
         return from_cuda(launch_linear_w4a16_mma(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd, d_flags,
                                                  (cudaStream_t)stream));
-    return from_cuda(launch_linear_w4a16(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd,
+    return from_cuda(launch_linear_w4a16(x, (int)dt, T, K, ldx, q, scales, d_s2, N, (int)out_dt, out, ldd, d_flags,
                                          (cudaStream_t)stream));
 }
 

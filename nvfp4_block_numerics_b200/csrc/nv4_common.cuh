@@ -38,6 +38,14 @@ __device__ __forceinline__ void flag_or(uint32_t* flags, uint32_t bits)
     if (flags != nullptr && bits != 0u) atomicOr(flags, bits);
 }
 
+// Whether a value is a NaN or an Inf, gathered over many at one FMA each: 0 * v is NaN for just those.
+struct NonFinite {
+    float sum = 0.0f;
+
+    __device__ __forceinline__ void see(float v) { sum = fmaf(v, 0.0f, sum); }
+    __device__ __forceinline__ uint32_t flag() const { return sum == 0.0f ? 0u : kFlagNonFinite; }
+};
+
 // ---------------------------------------------------------------- BF16
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

@@ -100,7 +100,7 @@ constexpr int64_t kMaxFewRows = 16;
 bool few_rows_w4a16(int64_t T, int64_t K);
 cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
-                                cudaStream_t s);
+                                uint32_t* d_flags, cudaStream_t s);
 cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                     const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
                                     uint32_t* d_flags, cudaStream_t s);

@@ -32,6 +32,7 @@ struct LinearParams {
     uint32_t T, N, K;
     uint32_t z, xs_bytes, red_bytes;              // cluster size; shared memory of token rows, of warp sums
     uint32_t tile, ntile, wk;                     // rows per tile, tiles per cluster, warps per tile
+    uint32_t* d_flags;
 };
 
 template <int kDt, int kOut, bool kVec, int NT>
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     });
     Acc<NT> acc;
     clear<NT>(acc);
+    NonFinite odd;                                // among the outputs before they are rounded
     uint32_t ut = grp, uc = wig, buf = 0u;        // the step to multiply next
     ring.run(load, [&](const uint8_t* slot) {
         const uint4* xc = xs + (size_t)uc * 32u * m;
@@ -101,7 +103,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (r >= nr) continue;
             const float s = sum_parts<kTile>(first + r * (8 * NT) + tok, wk);
             if (p.z > 1u) part[(size_t)(a + r) * (8 * NT) + tok] = s * rows.descale[tok];
-            else store_out<kOut>(p.out, (int64_t)tok * p.ldd + r0 + a + r, s * s2 * rows.descale[tok]);
+            else {
+                const float y = s * s2 * rows.descale[tok];
+                odd.see(y);
+                store_out<kOut>(p.out, (int64_t)tok * p.ldd + r0 + a + r, y);
+            }
         }
         buf ^= 1u;
         uc = wig;
@@ -117,10 +123,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             for (uint32_t q = 0; q < 8u; ++q) v[q] = q < p.z ? ld_dsmem_f32(part + (size_t)r * (8 * NT) + tok, q) : 0.0f;
 #pragma unroll
             for (uint32_t q = 0; q < 8u; ++q) s += v[q];
+            odd.see(s * s2);
             store_out<kOut>(p.out, (int64_t)tok * p.ldd + r0 + r, s * s2);
         }
         cluster_sync();                           // the others' sums have been read
     }
+    const uint32_t flags = __reduce_or_sync(0xFFFFFFFFu, odd.flag());
+    if (lane == 0u) flag_or(p.d_flags, flags);
 }
 
 template <int kDt, int kOut, bool kVec, int NT>
@@ -197,11 +206,12 @@ bool few_rows_w4a16(int64_t T, int64_t K) { return T <= kMaxFewRows && w4::stagi
 
 cudaError_t launch_linear_w4a16(const void* x, int dt, int64_t T, int64_t K, int64_t ldx, const uint8_t* q,
                                 const uint8_t* sc, const float* d_s2, int64_t N, int out_dt, void* out, int64_t ldd,
-                                cudaStream_t s)
+                                uint32_t* d_flags, cudaStream_t s)
 {
     using namespace w4;
     const Staging st = staging_of(T, K);
-    const LinearParams p{x, ldx, q, sc, d_s2, out, ldd, (uint32_t)T, (uint32_t)N, (uint32_t)K, st.z, st.bytes, 0u, 0u, 0u, 0u};
+    const LinearParams p{x, ldx, q, sc, d_s2, out, ldd, (uint32_t)T, (uint32_t)N, (uint32_t)K, st.z, st.bytes, 0u, 0u, 0u, 0u,
+                         d_flags};
     const bool vec = K % 64 == 0;                                  // (the scales are 16-byte aligned)
     if (dt == 0)
         return out_dt == 0 ? pick_linear<0, 0>(p, vec, s)

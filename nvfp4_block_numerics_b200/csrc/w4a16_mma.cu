@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     uint32_t flags = 0u;
+    NonFinite odd;                                                 // among the outputs before they are rounded
     auto aborted = [&]() { return *reinterpret_cast<volatile uint32_t*>(&sm.abort) != 0u; };
     auto give_up = [&]() { flags |= kFlagTimeout; atomicOr(&sm.abort, 1u); };
 
@@ -370,9 +371,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
                     float v[16];
                     tmem_ld16(taddr + c, v);
 #pragma unroll
-                    for (uint32_t k = 0; k < 16; ++k)
+                    for (uint32_t k = 0; k < 16; ++k) {
+                        odd.see(v[k] * s2);                        // (what lies outside the output is 0 s2, or NaN with all of it)
                         if (tok0 + c + k < p.T && n0 + lane < p.N)
                             static_cast<float*>(p.out)[(int64_t)(tok0 + c + k) * p.ldd + n0 + lane] = v[k] * s2;
+                    }
                 }
                 release();
             } else {
@@ -382,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
                 for (uint32_t c = 0; c < kCols; c += 16u) {
                     float v[16];
                     tmem_ld16(taddr + c, v);
+#pragma unroll
+                    for (uint32_t k = 0; k < 16; ++k) odd.see(v[k] * s2);
 #pragma unroll
                     for (uint32_t k = 0; k < 8; ++k)
                         w[c / 2 + k] = (uint32_t)to16<kOut>(v[2 * k] * s2) | (uint32_t)to16<kOut>(v[2 * k + 1] * s2) << 16;
@@ -436,7 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
             if (cluster_any(&sm.abort, p.z)) continue;             // a CTA that gave up has no sums to add
 #pragma unroll
             for (uint32_t k = 0; k < 4u; ++k)
-                if (r + k < rows) store1<kOut>(p.out, (int64_t)(tok0 + tok) * p.ldd + n0 + r + k, o[k]);
+                if (r + k < rows) {
+                    odd.see(o[k]);
+                    store1<kOut>(p.out, (int64_t)(tok0 + tok) * p.ldd + n0 + r + k, o[k]);
+                }
         }
         cluster_sync();                                            // the others have read this CTA's sums
     }
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_mma_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(tmem, 512u);
     }
-    flags = __reduce_or_sync(0xFFFFFFFFu, flags);
+    flags = __reduce_or_sync(0xFFFFFFFFu, flags | odd.flag());
     if (lane == 0) flag_or(p.d_flags, flags);
 }
 
