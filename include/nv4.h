@@ -532,7 +532,9 @@ NV4_API nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int6
  * nothing (padded rows: out is 0 if a token has none); an id that a token names more than once
  * counts with the sum of its weights.  The hidden values are FP32; the down product takes them as
  * two FP16 parts, 22 bits (a relative error of 2^-22, or 2^-50 of their row's largest magnitude);
- * all sums are FP32; results do not depend on the order in which CTAs run.
+ * all sums are FP32; results do not depend on the order in which CTAs run.  A NaN or Inf in a token
+ * that has an expert makes all its outputs NaN or Inf, and no other token's; NV4_FLAG_NONFINITE is
+ * set if an output is NaN or Inf before it is rounded to out_dt.
  *
  * nv4_moe_layer -- both, one after the other.
  *

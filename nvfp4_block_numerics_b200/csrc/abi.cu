@@ -682,10 +682,12 @@ static nv4_status check_moe_experts(int64_t T, int64_t H, int64_t I, const nv4_e
 
 static MoeExpertsArgs moe_args(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
                                const float* weights, int top_k, int64_t E, int64_t I,
-                               const nv4_expert_weights* const w[3], nv4_dtype out_dt, void* out, int64_t ldd, void* work)
+                               const nv4_expert_weights* const w[3], nv4_dtype out_dt, void* out, int64_t ldd, void* work,
+                               uint32_t* d_flags)
 {
     return MoeExpertsArgs{x, (int)dt, (int)out_dt, T, top_k, E, H, I, ldx, ldd, ids, weights, w[0]->q, w[0]->scales,
-                          w[1]->q, w[1]->scales, w[2]->q, w[2]->scales, w[0]->d_s2, w[1]->d_s2, w[2]->d_s2, work, out};
+                          w[1]->q, w[1]->scales, w[2]->q, w[2]->scales, w[0]->d_s2, w[1]->d_s2, w[2]->d_s2, work, out,
+                          d_flags};
 }
 
 nv4_status nv4_moe_route(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const void* w_router,
@@ -713,13 +715,13 @@ nv4_status nv4_moe_experts(const void* x, nv4_dtype dt, int64_t T, int64_t H, in
                            const nv4_expert_weights* up, const nv4_expert_weights* down, nv4_dtype out_dt, void* out,
                            int64_t ldd, void* d_work, size_t work_bytes, uint32_t* d_flags, void* stream)
 {
-    (void)d_flags;
     const nv4_expert_weights* const w[3] = {gate, up, down};
     nv4_status st = check_moe_rows(x, dt, T, H, ldx, E, top_k);
     if (st == NV4_OK) st = check_moe_experts(T, H, I, w, ids, weights, top_k, out_dt, out, ldd, d_work, work_bytes);
     if (st != NV4_OK || T == 0) return st;
     return from_cuda(launch_moe_experts(
-        moe_args(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work), false, (cudaStream_t)stream));
+        moe_args(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work, d_flags), false,
+        (cudaStream_t)stream));
 }
 
 nv4_status nv4_moe_layer(const void* x, nv4_dtype dt, int64_t T, int64_t H, int64_t ldx, const void* w_router,
@@ -734,7 +736,7 @@ nv4_status nv4_moe_layer(const void* x, nv4_dtype dt, int64_t T, int64_t H, int6
     if (st != NV4_OK || T == 0) return st;
     if (w_router == nullptr) return NV4_ERR_NULL;
     if (!aligned16(w_router)) return NV4_ERR_ALIGN;
-    const MoeExpertsArgs a = moe_args(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work);
+    const MoeExpertsArgs a = moe_args(x, dt, T, H, ldx, ids, weights, top_k, E, I, w, out_dt, out, ldd, d_work, d_flags);
     st = from_cuda(launch_moe_route(x, (int)dt, T, H, ldx, w_router, E, top_k, renormalize != 0, ids, weights, &a, d_flags,
                                     (cudaStream_t)stream));
     if (st != NV4_OK) return st;

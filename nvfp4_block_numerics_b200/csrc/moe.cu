@@ -294,6 +294,7 @@ struct Experts {
     void* out;
     int64_t ldd;
     uint32_t T, k, E, H, I;
+    uint32_t* d_flags;
 };
 
 // (What a kernel in front on the stream wrote is read with coherent loads: a CTA may have started
@@ -701,13 +702,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     });
     __syncthreads();
     // ---- the warps' sums of a tile, in warp order
+    NonFinite odd;                                                 // among the outputs before they are rounded
     for (uint32_t i = tid; i < p.T * R; i += kThreads) {
         const uint32_t tok = i / R, r = i - tok * R, tl = r / th, in = r - tl * th;
         float v = 0.0f;
 #pragma unroll 4
         for (uint32_t w = 0; w < wpt; ++w) v += Yall[((size_t)(w * ntile + tl) * p.T + tok) * 16u + in];
+        odd.see(v);
         w4::store_out<kOut>(p.out, (int64_t)tok * p.ldd + r0 + r, v);
     }
+    const uint32_t flags = __reduce_or_sync(0xFFFFFFFFu, odd.flag());
+    if (lane == 0u) flag_or(p.d_flags, flags);
 }
 
 template <class Kern, class P>
@@ -811,7 +816,7 @@ cudaError_t launch_moe_experts(const MoeExpertsArgs& a, bool routed, cudaStream_
     size_t n;
     const Experts p{a.x, a.ldx, a.ids, a.weights, a.gq, a.gs, a.uq, a.us, a.dq, a.ds, a.g2, a.u2, a.d2,
                     work_of(a.work, (size_t)a.T, (size_t)a.k, (size_t)a.H, (size_t)a.I, &n), a.out, a.ldd,
-                    (uint32_t)a.T, (uint32_t)a.k, (uint32_t)a.E, (uint32_t)a.H, (uint32_t)a.I};
+                    (uint32_t)a.T, (uint32_t)a.k, (uint32_t)a.E, (uint32_t)a.H, (uint32_t)a.I, a.d_flags};
     if (!routed) {
         if (a.dt == 0) moe_rows_kernel<0><<<(unsigned)a.T, 512, 0, s>>>(a.x, a.ldx, p.H, p.work);
         else moe_rows_kernel<1><<<(unsigned)a.T, 512, 0, s>>>(a.x, a.ldx, p.H, p.work);

@@ -118,6 +118,7 @@ struct MoeExpertsArgs {
     const float *g2, *u2, *d2;
     void* work;
     void* out;
+    uint32_t* d_flags;
 };
 size_t moe_work_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
 cudaError_t launch_moe_route(const void* x, int dt, int64_t T, int64_t H, int64_t ldx, const void* wr, int64_t E,
