@@ -489,7 +489,7 @@ static cudaError_t run(Params& p, cudaStream_t s)
     const uint32_t sms = (uint32_t)num_sms();
     // every CTA keeps a chunk; a wave beside its chunks (launch, first loads, the cluster's sums): some
     // 3 chunks' time.  With more tiles than SMs a CTA walks several unsplit, the next one's loads under
-    // the last one's stores (1000 x 2880 x 2880, 184 tiles: 38 us, 52 in clusters of 2).  (The sums of
+    // the last one's stores (1000 x 2880 x 2880 on tiles of 128, 184 of them: 38 us, 52 in clusters of 2).  (The sums of
     // 256 token columns would leave nothing of x's stages to spare.)
     p.z = kTok <= 128 && p.tiles <= sms ? split_tiles(kern, kThreads, smem, p.tiles, p.chunks, 1u, 3u, fits, dev) : 1u;
     cudaLaunchConfig_t cfg = {};
@@ -540,11 +540,18 @@ cudaError_t launch_linear_w4a16_mma(const void* x, int dt, int64_t T, int64_t K,
     p.vec = ldd % 8 == 0 ? 1u : 0u;
     p.d_flags = d_flags;
     const uint32_t sms = (uint32_t)num_sms();
-    // the widest token tile that the rows fill; half of it where that leaves SMs without a tile
+    // the widest token tile that the rows fill, but 128 instead of 256 while those tiles fit the SMs at once (they
+    // can split K then), or where they cost less: waves x (stages + a tile's end) + what a launch costs, in stages
+    // of some 0.34 us, which hardly depend on the width.  128 / 256, us: 300 x 8192 x 8192 93.6 / 51.8, 1000 x
+    // 2880 x 2880 37.3 / 26.0, 256 x 16384 x 2048 30.9 / 21.5, 600 x 4096 x 1024 17.0 / 13.9; 600 x 2880 x 2880
+    // 21.7 / 25.6, 512 x 4096 x 4096 29.5 / 30.9, 800 x 5000 x 512 13.1 / 19.9.
     uint32_t tok = T <= 32 ? 32u : T <= 64 ? 64u : T <= 128 ? 128u : 256u;
-    auto tiles = [&](uint32_t k) { return p.n_tiles * (uint32_t)((T + k - 1) / k); };
-    if (tok == 256u && tiles(256u) < sms) tok = 128u;
-    p.tiles = tiles(tok);
+    auto tiles = [&](uint32_t k) { return (uint64_t)p.n_tiles * (uint64_t)((T + k - 1) / k); };
+    if (tok == 256u) {
+        const uint64_t stages = (uint64_t)(K + 63) / 64, narrow = (tiles(128u) + sms - 1u) / sms, wide = (tiles(256u) + sms - 1u) / sms;
+        if (narrow == 1u || narrow * (stages + 2u) + 20u <= wide * (stages + stages / 20u + 6u) + 28u) tok = 128u;
+    }
+    p.tiles = (uint32_t)tiles(tok);
     if (!x_map(&p.map_x, x, dt, T, K, ldx, tok)) return cudaErrorInvalidValue;
     const bool vec = K % 64 == 0;                                  // (16-byte aligned codes, 4-byte aligned scales)
     if (tok == 32u) return pick<32>(p, dt, out_dt, vec, s);
