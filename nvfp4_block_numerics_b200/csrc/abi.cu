@@ -22,6 +22,7 @@ int num_sms()
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0u; }
 
 static nv4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NV4_OK : NV4_ERR_CUDA; }
 
@@ -637,7 +638,8 @@ nv4_status nv4_linear_w4a16(const void* x, nv4_dtype dt, int64_t T, int64_t K, i
     if (T == 0 || N == 0) return NV4_OK;
     if (K == 0) return NV4_ERR_SHAPE;
     if (x == nullptr || q == nullptr || scales == nullptr || d_s2 == nullptr || out == nullptr) return NV4_ERR_NULL;
-    if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned16(out) || ldx % 8 != 0) return NV4_ERR_ALIGN;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned4(d_s2) || !aligned16(out) || ldx % 8 != 0)
+        return NV4_ERR_ALIGN;
     if (K > kMaxW4K || T >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || ((T + 31) / 32) * ((N + 127) / 128) >= (int64_t)1 << 31)
         return NV4_ERR_LIMIT;
     if (!few_rows_w4a16(T, K))
@@ -659,8 +661,6 @@ static nv4_status check_moe_rows(const void* x, nv4_dtype dt, int64_t T, int64_t
     if (!aligned16(x) || ldx % 8 != 0) return NV4_ERR_ALIGN;
     return NV4_OK;
 }
-
-static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0u; }
 
 static nv4_status check_moe_experts(int64_t T, int64_t H, int64_t I, const nv4_expert_weights* const w[3],
                                     const int32_t* ids, const float* weights, int top_k, nv4_dtype out_dt, const void* out,
