@@ -374,6 +374,10 @@ __device__ __forceinline__ void build_lists(Lists& L, const Experts& p)
     __syncthreads();
 }
 
+// A sum of scaled rows times what undoes the row's scale (a power of two) and times scale_2, the one below 1
+// first: neither the sum times a large one nor the product of two small ones leaves FP32 where the result does not.
+__device__ __forceinline__ float two_scales(float sum, float d, float s2) { return d < 1.0f ? sum * d * s2 : sum * s2 * d; }
+
 // ---------------------------------------------------------------- gate, up, SwiGLU
 constexpr uint32_t kMaxSegs = 8;
 
@@ -494,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
                 const uint32_t r = i & 15u, col = i >> 4, hr = sg.f0 + col, at_r = (r >> 3) * 128u + (r & 7u) * 8u + col;
                 if (r >= nr) continue;
                 const float ds = descale[L.tok[hr]];
-                const float gv = w4::sum_parts<kTile>(first + at_r, wk) * s_gate * ds;
-                const float uv = w4::sum_parts<kTile>(first + at_r + 64u, wk) * s_up * ds;
+                const float gv = two_scales(w4::sum_parts<kTile>(first + at_r, wk), ds, s_gate);
+                const float uv = two_scales(w4::sum_parts<kTile>(first + at_r + 64u, wk), ds, s_up);
                 p.work.h[(size_t)hr * p.I + sg.i0 + a + r] = gv / (1.0f + expf(-gv)) * uv;
             }
             uc = wig;
@@ -586,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Lists L;
     float* Yall = reinterpret_cast<float*>(smem + w4::kRing);      // [16 warps][T][16]
-    // of a row of h: its scale, routing weight x expert scale (one product of the three, of a row near 2^-110
-    // say, could be subnormal where the result is not); as many as there are pairs, the rest of the SM is L1's
+    // of a row of h: its scale, routing weight x expert scale, in the order of two_scales; as many as there are pairs, the
+    // rest of the SM is L1's
     float2* coef = reinterpret_cast<float2*>(Yall + (size_t)kWarps * p.T * 16u);
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const uint32_t r0 = (uint32_t)((uint64_t)blockIdx.x * p.H / gridDim.x);
@@ -641,7 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     ring.begin(smem + warp * (w4::kDepth * w4::kSlot), steps, load);
     w4::pdl_wait();                                                // h is complete
     __syncthreads();                                               // coef
-    for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) coef[i].x = p.work.hd[i];
+    for (uint32_t i = tid; i < (uint32_t)L.first[L.n]; i += kThreads) {
+        const float d = p.work.hd[i], c = coef[i].y;
+        coef[i] = d < 1.0f ? make_float2(d, c) : make_float2(c, d);
+    }
     __syncthreads();
     w4::AccOf<2, 2> acc;                                           // [chain][part of h]
     w4::clear<2, 2>(acc);

@@ -79,7 +79,7 @@ def test_hidden_values_keep_their_bits(dt, T, E, H, I):
 
 
 @pytest.mark.parametrize("T", [2, 7])
-@pytest.mark.parametrize("s_up,s_down", [(-80, -55), (80, 40), (-60, 30), (0, 0)])
+@pytest.mark.parametrize("s_up,s_down", [(-80, -55), (80, 40), (-60, 30), (0, 0), (110, -60)])
 def test_scales_far_from_one(T, s_up, s_down):
     """Hidden values and scale_2 of extreme magnitudes whose product is an ordinary number: the sum is exact, the
     routing weight times scale_2 is exact (0.7 times a power of two), so one rounding is left, 2^-24, or 2^-150 where the
