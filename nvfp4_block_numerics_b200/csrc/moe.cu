@@ -7,8 +7,9 @@
 //            (ties: the lower index); weight = p, or p / sum of the chosen p
 //   experts  h = silu(gate_e x) * (up_e x);  y[t] = sum_j weight[t, j] * down_e h
 //
-// Four launches, each a programmatic dependent of the one before: its CTAs start, and do what
-// does not depend on it, while the last CTAs in front finish.
+// Four launches, each a programmatic dependent of the one before.  Gate / up fills an SM's register file and
+// down most of it, so that on an SM their prologues (lists, first weights) begin once the kernel in front
+// has left it, not under it; only the router's and the small kernels' CTAs share one.
 //   * moe_route_kernel: a 16-CTA cluster per one or two tokens.  The products are exact and are summed in
 //     FP64, so that the choice of experts is that of the exact logits unless two of them lie within the
 //     sums' rounding (2^-53 of the sum of magnitudes, per addition).  For BF16 that takes FP64 products (formed
@@ -27,9 +28,10 @@
 // The floor is reading the chosen experts' weights once from HBM; both products (nv4_w4.cuh) split
 // their rows evenly over the SMs, to one row, and read the token rows through L1.  An expert with
 // more than 8 tokens is multiplied in passes of 8.
-// 64 experts of 1536 x 4096, 8 per token: 1 token 44 us (85 MB; router 7, gate / up 22, hidden 3, down
-// 16, overlapped), 48 tokens 220 us (680 MB; 13, 117, 4, 84).  Bound, 48 tokens: decoding on the issue
-// slots (54% gate / up, 49% down) and L1 (52%, 56%) at 3.9 and 2.7 TB/s; 1 token: four launches' latencies.
+// 64 experts of 1536 x 4096, 8 per token: 1 token 38.7 us on the device, 45 a call (85 MB; by itself, from a cold
+// L2, router 9, gate / up 24, hidden 5, down 18), 48 tokens 257 us either way (680 MB; 16, 118, 5.5, 111).
+// Bound, 48 tokens: decoding on the issue slots (54% gate / up, 43% down) and L1 (52%, 61%) at 3.9 and 2.1 TB/s
+// (the second part of h costs down 27 of its 111 us); 1 token: four launches' latencies.
 #include <cfloat>
 
 #include "nv4_async.cuh"
@@ -661,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             if (us >= L.sub[ua + 1u]) ++ua;
             f0 = L.first[ua] + (us - L.sub[ua]) * kPass;
             m = min(kPass, L.first[ua + 1u] - f0);
-            // up to 4 rows: both parts of a row are columns of one MMA, 4 apart
+            // up to 4 rows: both parts of a row are columns of one MMA, 4 apart (8 tokens of 64 experts 129 us, with
+            // two MMAs 140; 1 token 38.9, 40.2; 48 tokens 258, 262)
             paired = m <= 4u;
             const uint32_t col = paired ? g & 3u : g;
             xr = p.work.h16 + 2u * (size_t)(f0 + min(col, m - 1u)) * part + (paired && g >= 4u ? part : 0u);

@@ -23,8 +23,9 @@
 //     through a 2 KB transpose per warp so that a store covers 64 bytes of an output row.
 // With few tiles a cluster of z CTAs shares one: each multiplies its part of K, the partial sums
 // meet through distributed shared memory and are added in rank order.
-// Bound: the tensor pipe and the decoders together (4096 x 16384 x 2048: 210 us, 1.31 PFLOP/s, 80% of a
-// BF16 library product at its burst rate; tensor pipe 65%, issue slots 50%).  The decoders' rate per
+// Bound: the tensor pipe and the decoders together (4096 x 16384 x 2048: 214 us back to back, 1.28 PFLOP/s, 79% of
+// a BF16 library product at its burst rate, and 247 us, 1.11 PFLOP/s, among other passes with new inputs; tensor
+// pipe 64%, issue slots 50%).  The decoders' rate per
 // stage is the same whatever kTok is, so 17 rows cost nearly what 128 do (2880 x 2880: 9.9 and 12.5 us).
 // Every mbarrier wait is bounded (kWaitLimitNs), as in gemm.cu.
 #include <type_traits>
